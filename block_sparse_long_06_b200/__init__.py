@@ -22,14 +22,17 @@ LIB_PATH = os.path.join(_HERE, "libbsa.so")
 BSA_OK, BSA_ERR_INVALID_ARG, BSA_ERR_UNSUPPORTED, BSA_ERR_WORKSPACE, BSA_ERR_CUDA = range(5)
 BSA_DEV_BAD_PAGE, BSA_DEV_BAD_KEPT, BSA_DEV_NONFINITE, BSA_DEV_TIMEOUT, BSA_DEV_FP16_RANGE = (
     0x1, 0x2, 0x4, 0x8, 0x10)
+BSA_DEV_BAD_LENGTH = 0x20
 PHASE_DECODE, PHASE_PREFILL = 0, 1
 OP_SCORE, OP_SELECT, OP_DECODE, OP_PREFILL, OP_PBS_PERMUTE = 0, 1, 2, 3, 4
+OP_ATTEND_PACKED, OP_DECODE_SHARED = 5, 6
 BLOCK = 64
 
 EXPORTED = ["bsa_max_kept", "bsa_workspace_size", "bsa_score_blocks", "bsa_select_top_p",
             "bsa_decode", "bsa_prefill", "bsa_status_string", "bsa_last_cuda_error",
             "bsa_decode_noalloc", "bsa_quantize_index_keys", "bsa_score_blocks_q",
-            "bsa_pbs_permute"]
+            "bsa_pbs_permute", "bsa_norm_rope", "bsa_append_kv", "bsa_attend_packed",
+            "bsa_decode_shared", "bsa_packed_workspace_size"]
 NOALLOC_SCRATCH_BYTES = 8 << 20
 IDX_FP4, IDX_INT4 = 1, 2
 QIDX_RECORD_BYTES = 576
@@ -68,6 +71,24 @@ class CProblem(ctypes.Structure):
                 ("kept_groups", ctypes.c_void_p)]
 
 
+class CRows(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("type", ctypes.c_int32)]
+
+
+class CTokens(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int32), ("B", ctypes.c_int32), ("Hq", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("r", ctypes.c_int32),
+                ("block", ctypes.c_int32), ("T", ctypes.c_int32),
+                ("cu_seqlens", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("rope_steps", ctypes.c_void_p),
+                ("rope_dim", ctypes.c_int32), ("rope_interleaved", ctypes.c_int32),
+                ("rope_factor", ctypes.c_float), ("norm", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("causal", ctypes.c_int32),
+                ("attn_scale", ctypes.c_float), ("q_stride", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -101,6 +122,16 @@ def load_library(path: str = LIB_PATH):
     lib.bsa_score_blocks_q.restype = ctypes.c_int
     lib.bsa_pbs_permute.argtypes = [P, vp, CCache, CCache, CCache, vp, vp, vp, vp, vp, sz, vp, vp]
     lib.bsa_pbs_permute.restype = ctypes.c_int
+    TP = ctypes.POINTER(CTokens)
+    lib.bsa_norm_rope.argtypes = [TP, CRows, CRows, CRows, CRows, vp, vp]
+    lib.bsa_append_kv.argtypes = [TP, CRows, CRows, CRows, CCache, CCache, CCache, CRows, CRows,
+                                  vp, vp]
+    lib.bsa_attend_packed.argtypes = [TP, vp, CCache, CCache, vp, vp, vp, vp, sz, vp, vp]
+    lib.bsa_decode_shared.argtypes = [TP, vp, CCache, CCache, vp, vp, vp, vp, vp, vp, sz, vp, vp]
+    lib.bsa_packed_workspace_size.argtypes = [TP, ctypes.c_int32, ctypes.POINTER(sz)]
+    for name in ("bsa_norm_rope", "bsa_append_kv", "bsa_attend_packed", "bsa_decode_shared",
+                 "bsa_packed_workspace_size"):
+        getattr(lib, name).restype = ctypes.c_int
     lib.bsa_status_string.argtypes = [ctypes.c_int]
     lib.bsa_status_string.restype = ctypes.c_char_p
     lib.bsa_last_cuda_error.argtypes = []
@@ -243,6 +274,168 @@ def paged_qcache(num_pages: int, Hkv: int, page_table: torch.Tensor, fmt: int, d
     return QCache(rec, gs, fmt, 0, Hkv, 1, page_table, num_pages)
 
 
+# ------------------------------------------------------------------ new token rows
+def rope_frequencies(dim: int, theta: float = 10000.0, scaling: str = "none",
+                     factor: float = 1.0, original: int = 8192, low: float = 1.0,
+                     high: float = 32.0):
+    """Rotary frequencies (radians per position, float64 [dim / 2] on the host) and the factor
+    on cos and sin. theta^(-2i/dim), and for contexts `factor` times the `original` length:
+
+    * ``linear``: every frequency divided by `factor`;
+    * ``ntk``: theta raised to theta * factor^(dim / (dim - 2)), which divides the slowest
+      frequency by `factor` and leaves the fastest;
+    * ``ramp``: by the turns a pair makes over `original` positions: at most `low` turns:
+      divided by `factor`, at least `high`: as they are, a linear ramp between; the factor on
+      cos and sin is 0.1 ln(factor) + 1.
+    """
+    if dim <= 0 or dim % 2 or not theta > 0 or not factor >= 1:
+        raise BsaError("rope_frequencies: dim even and > 0, theta > 0, factor >= 1")
+    i = torch.arange(dim // 2, dtype=torch.float64) * 2 / dim
+    if scaling == "none":
+        return theta ** -i, 1.0
+    if scaling == "linear":
+        return theta ** -i / factor, 1.0
+    if scaling == "ntk":
+        if dim == 2:
+            raise BsaError("rope_frequencies: ntk needs more than one pair")
+        return (theta * factor ** (dim / (dim - 2))) ** -i, 1.0
+    if scaling == "ramp":
+        if not 0 <= low < high:
+            raise BsaError("rope_frequencies: 0 <= low < high")
+        f = theta ** -i
+        keep = ((original * f / (2 * math.pi) - low) / (high - low)).clamp(0.0, 1.0)
+        return f * keep + f / factor * (1.0 - keep), 0.1 * math.log(factor) + 1.0
+    raise BsaError(f"rope_frequencies: unknown scaling {scaling!r}")
+
+
+def rope_steps(frequencies: torch.Tensor) -> torch.Tensor:
+    """What each pair turns by per position, in units of 2^-64 turns (int64, modulo 2^64)."""
+    turns = torch.remainder(frequencies.detach().double() / (2 * math.pi), 1.0)
+    high = torch.floor(turns * 2.0 ** 32)
+    low = torch.floor((turns * 2.0 ** 32 - high) * 2.0 ** 32)
+    high, low = high.to(torch.int64), low.to(torch.int64)
+    return torch.where(high >= 2 ** 31, high - 2 ** 32, high) * 2 ** 32 + low
+
+
+@dataclass
+class Rope:
+    """Rotary positions of the leading 2 * len(steps) elements of each head: pairs
+    (i, i + half) or, interleaved, (2i, 2i + 1). `steps` is a device int64 tensor
+    (rope_steps); `factor` multiplies cos and sin."""
+    steps: torch.Tensor
+    interleaved: bool = False
+    factor: float = 1.0
+
+    @classmethod
+    def make(cls, dim: int, theta: float = 10000.0, interleaved: bool = False, device="cuda",
+             **scaling) -> "Rope":
+        """Steps of rope_frequencies(dim, theta, **scaling), on `device`."""
+        f, factor = rope_frequencies(dim, theta, **scaling)
+        return cls(rope_steps(f).to(device), interleaved, factor)
+
+
+@dataclass
+class Tokens:
+    """Packed new token rows (bsa_tokens_t). Rows [cu_seqlens[b], cu_seqlens[b+1]) are the
+    newest tokens of sequence b, which has seq_lens[b] tokens with them; rows behind the last
+    sequence are padding."""
+    N: int
+    B: int
+    Hq: int
+    Hkv: int
+    d: int
+    T: int                                     # capacity: tokens of a sequence at most
+    cu_seqlens: Optional[torch.Tensor] = None  # device int32 [B+1]; None: N / B rows each
+    seq_lens: Optional[torch.Tensor] = None    # device int32 [B]; None: T each
+    positions: Optional[torch.Tensor] = None   # device int32 [N]; None: the token number
+    rope: Optional[Rope] = None
+    norm: bool = False
+    eps: float = 1e-6
+    q_weight: Optional[torch.Tensor] = None    # device float32 [d]; None: ones
+    k_weight: Optional[torch.Tensor] = None
+    causal: bool = True
+    attn_scale: float = 0.0                    # 0 -> 1/sqrt(d)
+    q_stride: int = 0                          # elements between tokens of q; 0 -> Hq * d
+    r: int = 16
+    block: int = BLOCK
+
+    def c(self) -> CTokens:
+        _want("cu_seqlens", self.cu_seqlens, torch.int32, (self.B + 1,))
+        _want("seq_lens", self.seq_lens, torch.int32, (self.B,))
+        _want("positions", self.positions, torch.int32, (self.N,))
+        _want("q_weight", self.q_weight, torch.float32, (self.d,))
+        _want("k_weight", self.k_weight, torch.float32, (self.d,))
+        rope, dim = self.rope, 0
+        if rope is not None:
+            _want("rope.steps", rope.steps, torch.int64, (rope.steps.numel(),))
+            dim = 2 * rope.steps.numel()
+        return CTokens(self.N, self.B, self.Hq, self.Hkv, self.d, self.r, self.block, self.T,
+                       _ptr(self.cu_seqlens), _ptr(self.seq_lens), _ptr(self.positions),
+                       None if rope is None else rope.steps.data_ptr(), dim,
+                       int(rope is not None and rope.interleaved),
+                       1.0 if rope is None else float(rope.factor), int(self.norm),
+                       float(self.eps), _ptr(self.q_weight), _ptr(self.k_weight),
+                       int(self.causal), float(self.attn_scale), int(self.q_stride))
+
+
+_ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _want(name, t, dtype, shape):
+    """Raise unless t is None or a contiguous device tensor of this type and shape."""
+    if t is None:
+        return
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise BsaError(f"{name}: contiguous {dtype} {tuple(shape)} wanted, got {t.dtype} "
+                       f"{tuple(t.shape)} with strides {t.stride()}")
+    if not t.is_cuda:
+        raise BsaError(f"{name}: has to be on the GPU")
+
+
+def _rows(name, t, N, heads, width, dtype=None) -> CRows:
+    """Head rows [N, heads, width] of any token and head stride; None: no rows."""
+    if t is None:
+        return CRows(None, 0, 0, 0)
+    if t.dtype not in _ROW_TYPES or (dtype is not None and t.dtype != dtype):
+        raise BsaError(f"{name}: {dtype or 'bfloat16, float16 or float32'} wanted, got {t.dtype}")
+    if tuple(t.shape) != (N, heads, width) or (width > 1 and t.stride(2) != 1):
+        raise BsaError(f"{name}: [{N}, {heads}, {width}] with contiguous heads wanted, got "
+                       f"{tuple(t.shape)} with strides {t.stride()}")
+    if not t.is_cuda:
+        raise BsaError(f"{name}: has to be on the GPU")
+    return CRows(t.data_ptr(), t.stride(0), t.stride(1), _ROW_TYPES[t.dtype])
+
+
+def _same_device(*tensors):
+    """The device of the tensors that are not None; raises when they differ."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise BsaError(f"tensors on {dev} and {t.device}")
+    return dev
+
+
+class _on:
+    """Make `device` the current one for a launch (streams and kernels belong to it)."""
+
+    def __init__(self, device):
+        self.device = device
+        self.before = -1
+
+    def __enter__(self):
+        now = torch.cuda.current_device()
+        if self.device.index != now:
+            self.before = now
+            torch.cuda.set_device(self.device)
+
+    def __exit__(self, *exc):
+        if self.before >= 0:
+            torch.cuda.set_device(self.before)
+
+
 # ------------------------------------------------------------------ the C entry points
 def bsa_max_kept(prob: Problem) -> int:
     return load_library().bsa_max_kept(ctypes.byref(prob.c()))
@@ -319,6 +512,98 @@ def bsa_pbs_permute(prob: Problem, q, k: Cache, v: Cache, k_idx: Cache, k_perm, 
                                           0 if workspace is None else workspace.numel(),
                                           _ptr(dev_status), _stream(stream)),
            "bsa_pbs_permute")
+
+
+def _token_tensors(tok: Tokens):
+    return (tok.cu_seqlens, tok.seq_lens, tok.positions, tok.q_weight, tok.k_weight,
+            None if tok.rope is None else tok.rope.steps)
+
+
+def bsa_norm_rope(tok: Tokens, q, q_out, k=None, k_out=None, dev_status=None, stream=None):
+    """Norm (tok.norm) and rotate (tok.rope) the heads of q [N, Hq, d] into q_out and of
+    k [N, Hkv, d] into k_out (bf16; either pair may be None, outputs may be the inputs)."""
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise BsaError("bsa_norm_rope: q and q_out, k and k_out come together")
+    dev = _same_device(q, q_out, k, k_out, dev_status, *_token_tensors(tok))
+    if dev is None:
+        raise BsaError("bsa_norm_rope: neither q nor k")
+    N, bf16 = tok.N, torch.bfloat16
+    args = (_rows("q", q, N, tok.Hq, tok.d), _rows("q_out", q_out, N, tok.Hq, tok.d, bf16),
+            _rows("k", k, N, tok.Hkv, tok.d), _rows("k_out", k_out, N, tok.Hkv, tok.d, bf16))
+    with _on(dev):
+        _check(load_library().bsa_norm_rope(ctypes.byref(tok.c()), *args, _ptr(dev_status),
+                                            _stream(stream)), "bsa_norm_rope")
+
+
+def bsa_append_kv(tok: Tokens, k, v, k_cache: Cache, v_cache: Cache, k_idx=None,
+                  kidx_cache: Optional[Cache] = None, q=None, q_out=None, dev_status=None,
+                  stream=None):
+    """Append k (normed and rotated) and v [N, Hkv, d] and, where given, the index keys
+    k_idx [N, Hkv, r] to their sequences' caches; q [N, Hq, d], where given, is normed and
+    rotated into q_out by the same launch."""
+    if (q is None) != (q_out is None) or (k_idx is None) != (kidx_cache is None):
+        raise BsaError("bsa_append_kv: q and q_out, k_idx and kidx_cache come together")
+    caches = [c for c in (k_cache, v_cache, kidx_cache) if c is not None]
+    dev = _same_device(k, v, k_idx, q, q_out, dev_status, *_token_tensors(tok),
+                       *(c.tensor for c in caches), *(c.page_table for c in caches))
+    N, d = tok.N, tok.d
+    args = (_rows("k", k, N, tok.Hkv, d), _rows("v", v, N, tok.Hkv, d),
+            _rows("k_idx", k_idx, N, tok.Hkv, tok.r), k_cache.c(), v_cache.c(),
+            CCache() if kidx_cache is None else kidx_cache.c(), _rows("q", q, N, tok.Hq, d),
+            _rows("q_out", q_out, N, tok.Hq, d, torch.bfloat16))
+    with _on(dev):
+        _check(load_library().bsa_append_kv(ctypes.byref(tok.c()), *args, _ptr(dev_status),
+                                            _stream(stream)), "bsa_append_kv")
+
+
+def bsa_packed_workspace_size(tok: Tokens, op: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().bsa_packed_workspace_size(ctypes.byref(tok.c()), op, ctypes.byref(out)),
+           "bsa_packed_workspace_size")
+    return out.value
+
+
+def _packed_call(name, tok, q, k, v, own, o, lse, o_f32, workspace, dev_status, stream):
+    dev = _same_device(q, k.tensor, v.tensor, k.page_table, v.page_table, *own, o, lse, o_f32,
+                       workspace, dev_status, *_token_tensors(tok))
+    N, Hq, d = tok.N, tok.Hq, tok.d
+    if q.dtype != torch.bfloat16 or tuple(q.shape) != (N, Hq, d) or not q.is_cuda or (
+            N > 0 and (q.stride(2) != 1 or q.stride(1) != d)):
+        raise BsaError(f"{name}: q has to be bfloat16 [{N}, {Hq}, {d}] on the GPU, a token's "
+                       f"heads side by side, got {q.dtype} {tuple(q.shape)} {q.stride()}")
+    c = tok.c()
+    if N > 1:
+        if tok.q_stride not in (0, q.stride(0)):
+            raise BsaError(f"{name}: q_stride {tok.q_stride}, but q has {q.stride(0)}")
+        c.q_stride = q.stride(0)
+    _want("o", o, torch.bfloat16, (N, Hq, d))
+    _want("lse", lse, torch.float32, (N, Hq))
+    _want("o_f32", o_f32, torch.float32, (N, Hq, d))
+    ptrs = [_ptr(q), k.c(), v.c()]
+    if name == "bsa_decode_shared":
+        _want("o_own", own[0], torch.float32, (N, Hq, d))
+        _want("lse_own", own[1], torch.float32, (N, Hq))
+        ptrs += [_ptr(own[0]), _ptr(own[1])]
+    with _on(dev):
+        _check(getattr(load_library(), name)(
+            ctypes.byref(c), *ptrs, _ptr(o), _ptr(lse), _ptr(o_f32), _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size(),
+            _ptr(dev_status), _stream(stream)), name)
+
+
+def bsa_attend_packed(tok: Tokens, q, k: Cache, v: Cache, o, lse, o_f32, workspace,
+                      dev_status=None, stream=None):
+    """Dense attention of packed rows q [N, Hq, d] over their sequences' caches."""
+    _packed_call("bsa_attend_packed", tok, q, k, v, (), o, lse, o_f32, workspace, dev_status,
+                 stream)
+
+
+def bsa_decode_shared(tok: Tokens, q, k: Cache, v: Cache, o_own, lse_own, o, lse, o_f32,
+                      workspace, dev_status=None, stream=None):
+    """Decode attention over shared prefixes (tok.B of them, caches k and v), joined with the
+    attention over each row's own tokens (o_own, lse_own; both None: none)."""
+    _packed_call("bsa_decode_shared", tok, q, k, v, (o_own, lse_own), o, lse, o_f32, workspace,
+                 dev_status, stream)
 
 
 def bsa_status_string(status: int) -> str:
@@ -427,6 +712,44 @@ class PbsPrefill:
         self.permute(q, k, v, k_idx, stream)
         self.pf.run(q, q_idx, contiguous_cache(self.kidx_perm), contiguous_cache(self.k_perm),
                     contiguous_cache(self.v_perm), stream)
+
+
+class _PackedBuffers:
+    def __init__(self, tok: Tokens, op: int, device, keep_f32):
+        dev = torch.device(device)
+        self.tok = tok
+        self.o = torch.empty(tok.N, tok.Hq, tok.d, dtype=torch.bfloat16, device=dev)
+        self.lse = torch.empty(tok.N, tok.Hq, dtype=torch.float32, device=dev)
+        self.o_f32 = (torch.empty(tok.N, tok.Hq, tok.d, dtype=torch.float32, device=dev)
+                      if keep_f32 else None)
+        ws = bsa_packed_workspace_size(tok, op)
+        self.workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+
+
+class PackedAttention(_PackedBuffers):
+    """Outputs and workspace for dense attention of packed rows. ``run`` enqueues
+    bsa_attend_packed on the current stream; lengths are read on the device, so the same
+    object (or a graph captured from ``run``) serves every batch of up to N rows."""
+
+    def __init__(self, tok: Tokens, device="cuda", keep_f32=True):
+        super().__init__(tok, OP_ATTEND_PACKED, device, keep_f32)
+
+    def run(self, q, k: Cache, v: Cache, stream=None):
+        bsa_attend_packed(self.tok, q, k, v, self.o, self.lse, self.o_f32, self.workspace,
+                          self.status, stream)
+
+
+class SharedPrefixDecode(_PackedBuffers):
+    """Outputs and workspace for decode over shared prefixes. ``run`` takes what a DecodeStep
+    over each sequence's own tokens left in its o_f32 and lse, or nothing."""
+
+    def __init__(self, tok: Tokens, device="cuda", keep_f32=True):
+        super().__init__(tok, OP_DECODE_SHARED, device, keep_f32)
+
+    def run(self, q, k: Cache, v: Cache, o_own=None, lse_own=None, stream=None):
+        bsa_decode_shared(self.tok, q, k, v, o_own, lse_own, self.o, self.lse, self.o_f32,
+                          self.workspace, self.status, stream)
 
 
 def problem_for(w, seq_lens: Optional[torch.Tensor] = None,

@@ -2,6 +2,7 @@
 // creation and kernel launches. No allocation, no synchronisation.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -195,6 +196,188 @@ bsa::CacheView qview(const bsa_qcache_t& c) {
   v.num_pages = c.num_pages;
   v.extent = c.extent;
   return v;
+}
+
+// ---------------------------------------------------------------- new token rows
+// Shape checks of a bsa_tokens_t.
+bsa_status_t check_tokens(const bsa_tokens_t* t) {
+  if (t == nullptr) return BSA_ERR_INVALID_ARG;
+  if (t->N < 0 || t->B <= 0 || t->Hq <= 0 || t->Hkv <= 0 || t->T < 0) return BSA_ERR_INVALID_ARG;
+  if (t->Hq % t->Hkv != 0) return BSA_ERR_INVALID_ARG;
+  if (t->cu_seqlens == nullptr && t->N % t->B != 0) return BSA_ERR_INVALID_ARG;
+  if (!std::isfinite(t->rope_factor) || !std::isfinite(t->eps) || !std::isfinite(t->attn_scale))
+    return BSA_ERR_INVALID_ARG;
+  if (t->eps < 0.f || t->attn_scale < 0.f) return BSA_ERR_INVALID_ARG;
+  if ((t->norm != 0 && t->norm != 1) || (t->causal != 0 && t->causal != 1) ||
+      (t->rope_interleaved != 0 && t->rope_interleaved != 1))
+    return BSA_ERR_INVALID_ARG;
+  if (t->rope_dim < 0 || t->rope_dim > t->d || (t->rope_dim > 0 && t->rope_steps == nullptr))
+    return BSA_ERR_INVALID_ARG;
+  if (t->q_stride < 0 || t->q_stride % 8 != 0) return BSA_ERR_INVALID_ARG;
+  if (t->block != 64 || t->r != 16) return BSA_ERR_UNSUPPORTED;
+  if (t->d != 64 && t->d != 128) return BSA_ERR_UNSUPPORTED;
+  if (t->rope_dim % 16 != 0) return BSA_ERR_UNSUPPORTED;
+  if (nblocks(t->T) > 32768) return BSA_ERR_UNSUPPORTED;
+  return BSA_OK;
+}
+
+// Head rows of type `type`: every head starts on a 16-byte boundary.
+bsa_status_t check_rows(const bsa_rows_t& x, int type) {
+  if (x.base == nullptr || !aligned16(x.base) || x.type != type) return BSA_ERR_INVALID_ARG;
+  const int64_t unit = type == BSA_TYPE_F32 ? 4 : 8;
+  if (x.token_stride < 0 || x.head_stride < 0 || x.token_stride % unit || x.head_stride % unit)
+    return BSA_ERR_INVALID_ARG;
+  return BSA_OK;
+}
+
+// An output that starts where its input does has to be the same rows.
+bool same_or_apart(const bsa_rows_t& in, const bsa_rows_t& out) {
+  return in.base != out.base || (in.type == out.type && in.token_stride == out.token_stride &&
+                                 in.head_stride == out.head_stride);
+}
+
+// Cache checks for a capacity of T tokens (see check_cache).
+bsa_status_t check_token_cache(const bsa_cache_t& c, const bsa_tokens_t* t, int width, bool rows_tma) {
+  bsa_problem_t p{};
+  p.T = t->T;
+  return check_cache(c, &p, width, rows_tma);
+}
+
+bsa::RowsView rows_view(const bsa_rows_t& x) {
+  bsa::RowsView v;
+  v.base = x.base;
+  v.token_stride = x.token_stride;
+  v.head_stride = x.head_stride;
+  return v;
+}
+
+// Fields shared by bsa_norm_rope and bsa_append_kv.
+bsa::HeadsArgs heads_args(const bsa_tokens_t* t, int type, int32_t* dev_status) {
+  bsa::HeadsArgs a{};
+  a.cu = t->cu_seqlens;
+  a.seq_lens = t->seq_lens;
+  a.positions = t->positions;
+  a.rope_steps = t->rope_steps;
+  a.norm = t->norm;
+  a.q_weight = t->norm ? t->q_weight : nullptr;
+  a.k_weight = t->norm ? t->k_weight : nullptr;
+  a.eps = t->eps;
+  a.status = dev_status;
+  a.N = t->N;
+  a.B = t->B;
+  a.Hq = t->Hq;
+  a.Hkv = t->Hkv;
+  a.d = t->d;
+  a.T = t->T;
+  a.type = type;
+  a.rope_dim = t->rope_dim;
+  a.rope_interleaved = t->rope_interleaved;
+  a.rope_factor = t->rope_factor == 0.f ? 1.0f : t->rope_factor;
+  return a;
+}
+
+// Workspace of the packed attention. Splits of the key axis: enough for about four units
+// an SM when the rows fill as few units as they can.
+struct PackedWorkspace {
+  int smax, max_entries;
+  size_t offs, entries, row_splits, ml, o, total;
+};
+PackedWorkspace packed_workspace(const bsa_tokens_t* t, bool shared, int num_sms) {
+  PackedWorkspace w;
+  const int per = bsa::packed_unit_tokens(t->Hq / t->Hkv);
+  const int64_t rows = t->N > 0 ? t->N : 1;
+  const int64_t least = (rows + per - 1) / per;
+  const int64_t want = (4ll * num_sms + least * t->Hkv - 1) / (least * t->Hkv);
+  const int64_t steps = (t->T + 127) / 128;
+  w.smax = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, 64), steps)));
+  w.max_entries = static_cast<int>((least + std::min<int64_t>(rows, t->B)) * w.smax);
+  w.offs = 256;
+  w.entries = w.offs + align256((static_cast<size_t>(t->B) + 1) * sizeof(int32_t));
+  w.row_splits = w.entries + align256(static_cast<size_t>(w.max_entries) * 2 * sizeof(int4));
+  w.ml = w.row_splits + align256(static_cast<size_t>(rows) * sizeof(int32_t));
+  const size_t parts = w.smax > 1 || shared ? static_cast<size_t>(w.smax) * rows * t->Hq : 0;
+  w.o = w.ml + align256(parts * 2 * sizeof(float));
+  w.total = w.o + align256(parts * t->d * sizeof(float));
+  return w;
+}
+
+// 3-D map over q [N, Hq, d] (bf16, `stride` elements a token): boxes of the G heads of one
+// kv group for 128 / G tokens, 64 elements wide, 128-byte swizzle. The box's rows lie in
+// shared memory as (token, head).
+bool make_q_map(CUtensorMap* m, const void* q, const bsa_tokens_t* t, int64_t stride) {
+  auto enc = get_encode();
+  if (!enc) return false;
+  const int G = t->Hq / t->Hkv;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(t->d), static_cast<cuuint64_t>(t->Hq),
+                        static_cast<cuuint64_t>(t->N)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(t->d) * 2, static_cast<cuuint64_t>(stride) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(128 / G)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box,
+                   estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+bsa_status_t packed_attention(const bsa_tokens_t* t, bool shared, const void* q, const bsa_cache_t& k,
+                              const bsa_cache_t& v, const float* o_own, const float* lse_own, void* o,
+                              float* lse, float* o_f32, void* workspace, size_t workspace_bytes,
+                              int32_t* dev_status, void* stream) {
+  bsa_status_t st = check_tokens(t);
+  if (st != BSA_OK) return st;
+  if (!is_pow2_group(t->Hq / t->Hkv)) return BSA_ERR_UNSUPPORTED;
+  if (t->N == 0) return BSA_OK;
+  if (q == nullptr || o == nullptr || lse == nullptr) return BSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(o_f32) || !aligned16(o_own))
+    return BSA_ERR_INVALID_ARG;
+  if ((o_own == nullptr) != (lse_own == nullptr)) return BSA_ERR_INVALID_ARG;
+  const int64_t stride = t->q_stride > 0 ? t->q_stride : static_cast<int64_t>(t->Hq) * t->d;
+  if (stride < static_cast<int64_t>(t->Hq) * t->d) return BSA_ERR_INVALID_ARG;
+  if ((st = check_token_cache(k, t, t->d, true)) != BSA_OK) return st;
+  if ((st = check_token_cache(v, t, t->d, true)) != BSA_OK) return st;
+  const int num_sms = num_sms_current();
+  const PackedWorkspace w = packed_workspace(t, shared, num_sms);
+  if (workspace == nullptr || workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return BSA_ERR_WORKSPACE;
+  CUtensorMap tq, tk, tv;
+  if (!make_q_map(&tq, q, t, stride) || !make_map(&tk, k.base, k.extent / t->d, t->d, false) ||
+      !make_map(&tv, v.base, v.extent / t->d, t->d, false))
+    return cuda_fail(cudaErrorInvalidValue);
+  bsa::PackedArgs a{};
+  char* ws = static_cast<char*>(workspace);
+  a.q = q;
+  a.k = view(k);
+  a.v = view(v);
+  a.cu = t->cu_seqlens;
+  a.seq_lens = t->seq_lens;
+  a.o_own = o_own;
+  a.lse_own = lse_own;
+  a.o = o;
+  a.lse = lse;
+  a.o_f32 = o_f32;
+  a.status = dev_status;
+  a.head = reinterpret_cast<int32_t*>(ws);
+  a.offs = reinterpret_cast<int32_t*>(ws + w.offs);
+  a.entries = reinterpret_cast<int4*>(ws + w.entries);
+  a.row_splits = reinterpret_cast<int32_t*>(ws + w.row_splits);
+  a.part_ml = reinterpret_cast<float*>(ws + w.ml);
+  a.part_o = reinterpret_cast<float*>(ws + w.o);
+  a.N = t->N;
+  a.B = t->B;
+  a.Hq = t->Hq;
+  a.Hkv = t->Hkv;
+  a.G = t->Hq / t->Hkv;
+  a.d = t->d;
+  a.T = t->T;
+  a.causal = shared ? 0 : t->causal;
+  a.smax = w.smax;
+  a.partial = shared ? 1 : 0;
+  a.max_entries = w.max_entries;
+  a.num_sms = num_sms;
+  a.scale_log2 = (t->attn_scale > 0.f ? t->attn_scale : 1.0f / std::sqrt(static_cast<float>(t->d))) *
+                 1.4426950408889634f;
+  const cudaError_t e = bsa::launch_packed(a, tq, tk, tv, num_sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? BSA_OK : cuda_fail(e);
 }
 
 // Workspace of bsa_pbs_permute: per-chunk row statistics, row log-sum-exps, importance.
@@ -588,6 +771,100 @@ bsa_status_t bsa_pbs_permute(const bsa_problem_t* p, const void* q, bsa_cache_t 
   const cudaError_t e =
       bsa::launch_pbs_permute(a, num_sms_current(), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? BSA_OK : cuda_fail(e);
+}
+
+bsa_status_t bsa_norm_rope(const bsa_tokens_t* t, bsa_rows_t q, bsa_rows_t q_out, bsa_rows_t k,
+                           bsa_rows_t k_out, int32_t* dev_status, void* stream) {
+  bsa_status_t st = check_tokens(t);
+  if (st != BSA_OK) return st;
+  if (t->N == 0) return BSA_OK;
+  if (q.base == nullptr && k.base == nullptr) return BSA_ERR_INVALID_ARG;
+  const int type = q.base != nullptr ? q.type : k.type;
+  if (type != BSA_TYPE_BF16 && type != BSA_TYPE_F16 && type != BSA_TYPE_F32)
+    return BSA_ERR_INVALID_ARG;
+  bsa::HeadsArgs a = heads_args(t, type, dev_status);
+  if (q.base != nullptr) {
+    if ((st = check_rows(q, type)) != BSA_OK || (st = check_rows(q_out, BSA_TYPE_BF16)) != BSA_OK)
+      return st;
+    if (!same_or_apart(q, q_out)) return BSA_ERR_INVALID_ARG;
+    a.q = rows_view(q);
+    a.q_out = rows_view(q_out);
+  }
+  if (k.base != nullptr) {
+    if ((st = check_rows(k, type)) != BSA_OK || (st = check_rows(k_out, BSA_TYPE_BF16)) != BSA_OK)
+      return st;
+    if (!same_or_apart(k, k_out)) return BSA_ERR_INVALID_ARG;
+    a.k = rows_view(k);
+    a.k_out = rows_view(k_out);
+  }
+  // a row's sequence says its position, or whether it is padding
+  a.needs_slot = t->cu_seqlens != nullptr || (t->positions == nullptr && t->rope_dim > 0);
+  const cudaError_t e =
+      bsa::launch_token_heads(a, num_sms_current(), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? BSA_OK : cuda_fail(e);
+}
+
+bsa_status_t bsa_append_kv(const bsa_tokens_t* t, bsa_rows_t k, bsa_rows_t v, bsa_rows_t kidx,
+                           bsa_cache_t k_cache, bsa_cache_t v_cache, bsa_cache_t kidx_cache,
+                           bsa_rows_t q, bsa_rows_t q_out, int32_t* dev_status, void* stream) {
+  bsa_status_t st = check_tokens(t);
+  if (st != BSA_OK) return st;
+  if (t->N == 0) return BSA_OK;
+  const int type = k.type;
+  if (type != BSA_TYPE_BF16 && type != BSA_TYPE_F16 && type != BSA_TYPE_F32)
+    return BSA_ERR_INVALID_ARG;
+  if ((st = check_rows(k, type)) != BSA_OK || (st = check_rows(v, type)) != BSA_OK) return st;
+  if ((st = check_token_cache(k_cache, t, t->d, true)) != BSA_OK) return st;
+  if ((st = check_token_cache(v_cache, t, t->d, true)) != BSA_OK) return st;
+  bsa::HeadsArgs a = heads_args(t, type, dev_status);
+  a.k = rows_view(k);
+  a.v = rows_view(v);
+  a.k_cache = view(k_cache);
+  a.v_cache = view(v_cache);
+  if (kidx.base != nullptr) {
+    if ((st = check_rows(kidx, type)) != BSA_OK) return st;
+    if ((st = check_token_cache(kidx_cache, t, t->r, false)) != BSA_OK) return st;
+    a.kidx = rows_view(kidx);
+    a.kidx_cache = view(kidx_cache);
+  }
+  if (q.base != nullptr) {
+    if ((st = check_rows(q, type)) != BSA_OK || (st = check_rows(q_out, BSA_TYPE_BF16)) != BSA_OK)
+      return st;
+    if (!same_or_apart(q, q_out)) return BSA_ERR_INVALID_ARG;
+    a.q = rows_view(q);
+    a.q_out = rows_view(q_out);
+  }
+  a.cached = 1;
+  a.needs_slot = 1;
+  const cudaError_t e =
+      bsa::launch_token_heads(a, num_sms_current(), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? BSA_OK : cuda_fail(e);
+}
+
+bsa_status_t bsa_packed_workspace_size(const bsa_tokens_t* t, int32_t op, size_t* bytes) {
+  if (bytes == nullptr) return BSA_ERR_INVALID_ARG;
+  *bytes = 0;
+  bsa_status_t st = check_tokens(t);
+  if (st != BSA_OK) return st;
+  if (op != BSA_OP_ATTEND_PACKED && op != BSA_OP_DECODE_SHARED) return BSA_ERR_INVALID_ARG;
+  if (!is_pow2_group(t->Hq / t->Hkv)) return BSA_ERR_UNSUPPORTED;
+  *bytes = packed_workspace(t, op == BSA_OP_DECODE_SHARED, num_sms_current()).total;
+  return BSA_OK;
+}
+
+bsa_status_t bsa_attend_packed(const bsa_tokens_t* t, const void* q, bsa_cache_t k, bsa_cache_t v,
+                               void* o, float* lse, float* o_f32, void* workspace,
+                               size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  return packed_attention(t, false, q, k, v, nullptr, nullptr, o, lse, o_f32, workspace,
+                          workspace_bytes, dev_status, stream);
+}
+
+bsa_status_t bsa_decode_shared(const bsa_tokens_t* t, const void* q, bsa_cache_t k, bsa_cache_t v,
+                               const float* o_own, const float* lse_own, void* o, float* lse,
+                               float* o_f32, void* workspace, size_t workspace_bytes,
+                               int32_t* dev_status, void* stream) {
+  return packed_attention(t, true, q, k, v, o_own, lse_own, o, lse, o_f32, workspace,
+                          workspace_bytes, dev_status, stream);
 }
 
 const char* bsa_status_string(bsa_status_t s) {

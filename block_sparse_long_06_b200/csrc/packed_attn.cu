@@ -1,0 +1,815 @@
+// Dense attention of packed query rows over paged or contiguous caches, on the
+// 5th-generation tensor cores: whole prompts and chunks of them (causal), single tokens,
+// and the rows of all sequences behind a shared prefix (not causal).
+//
+// For token row n of sequence b (token number p) and head h of kv group g:
+//   o = sum_j e^(s_j - m) v_j / l,  s_j = q.k_j * scale over the keys j <= p (causal) or all
+//   keys of the sequence, with the running maximum m and sum l in fp32 over one pass.
+//
+// Design:
+//  * The G query heads of a kv group are rows of the same tile: row r of a 128-row tile is
+//    token r / G, head r % G, which is how one TMA box {64, G, 128/G} of q [N, Hq, d] lands
+//    in shared memory. A unit is two such tiles (256/G tokens) of one kv head, so a key tile
+//    is read once for 256 rows, and a single token still fills G rows.
+//  * A step is 128 keys (two blocks of the cache). The loader warp copies K and V of a step
+//    into a ring of 32 KB stages; one issuing thread per tile runs S = Q K^T into the tile's
+//    128 columns of tensor memory and O += P V from it; 4 softmax warps per tile (one row a
+//    thread, so row maxima and sums need no shuffles) turn S into P, written as bf16 over S.
+//    The two tiles take turns: while one is in its softmax, the other has the tensor cores.
+//    P V (j) and S (j + 1) of a tile are issued by the same thread, in order, so S needs no
+//    second buffer and the arrival of S (j + 1) says that P V (j) is done.
+//  * The running maximum only moves when it grows by more than 8 (log2): O is then rescaled
+//    in tensor memory. P <= 2^8 is rounded to bf16 (half a step is 2^-9 of each term, below
+//    the 2^-9 rounding of the bf16 output once the terms' errors average); l sums the fp32
+//    values. V stays bf16, so no value range is lost.
+//  * Few rows over many keys: the plan kernel (one block) cuts units into splits of the key
+//    axis, until the SMs are filled; each writes its O, m and l in fp32 and the merge kernel
+//    joins them. Units are handed out longest first, one kv head after the other, so the
+//    SMs share one head's keys through L2 at a time.
+//  * Rows of V behind a sequence's end are whatever the page held before: a patch warp
+//    zeroes them in shared memory in the step that has the end (0 * NaN is NaN), before the
+//    step is handed to the tensor cores. K there may be anything: its scores are replaced.
+// Tensor memory: O of tile t at 128 t, S (and P) of tile t at 256 + 128 t. Every wait is
+// bounded; on a timeout the kernel reports BSA_DEV_TIMEOUT, drains and returns.
+#include "bsa_common.cuh"
+#include "bsa_internal.h"
+#include "tcgen05.cuh"
+
+namespace bsa {
+namespace {
+
+constexpr int kThreads = 384;          // warp 0 loads, 1-2 issue, 3 patches, 4-7 / 8-11 softmax
+constexpr int kWarpLoad = 0, kWarpMma = 1, kWarpPatch = 3, kWarpSm = 4;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kStep = 128;             // keys a step
+constexpr int kMaxStages = 10;
+constexpr int kPlanThreads = 1024;
+constexpr int kBuckets = 512;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D>
+struct Cfg {
+  static constexpr int kHalves = D / 64;            // 64-dim slabs (rows of 128 B)
+  static constexpr int kSlab = 128 * 128;           // 128 rows of one slab
+  static constexpr int kTile = kHalves * kSlab;     // 128 rows x D: a Q tile, or K or V of a step
+  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kOffKV = 2 * kTile;
+  static constexpr int kOffBar = kOffKV + kStages * kTile;
+};
+
+struct Unit {
+  int u, b, g, row0, ntok, pos0, len, step0, step1, split, nsplit, bad;
+};
+
+struct Bars {
+  uint64_t info_full[2], info_empty[2];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], kv_raw[kMaxStages];
+  uint64_t s_full[2], p_ready[2], o_full[2];
+  uint64_t mma_done[2];
+  Unit info[2];
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+template <int D>
+constexpr int smem_bytes() {
+  return Cfg<D>::kOffBar + static_cast<int>(sizeof(Bars)) + 1024;
+}
+static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory");
+
+BSA_DEVFN bool aborted(Bars* b) { return *reinterpret_cast<volatile int*>(&b->abort_flag) != 0; }
+BSA_DEVFN void set_abort(Bars* b, int32_t* status) {
+  *reinterpret_cast<volatile int*>(&b->abort_flag) = 1;
+  report(status, BSA_DEV_TIMEOUT);
+}
+
+BSA_DEVFN bool warp_wait(uint64_t* bar, uint32_t parity) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity);
+  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+
+BSA_DEVFN bool warp_wait_sleep(uint64_t* bar, uint32_t parity) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait_sleep(bar, parity);
+  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+
+BSA_DEVFN float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
+// Row (of width d) of the first token of block blk of (b, g), or -1 where it is bad.
+BSA_DEVFN int64_t block_row(const CacheView& c, int b, int g, int blk, int len, int d) {
+  int64_t phys = blk;
+  if (c.page_table != nullptr) {
+    phys = c.page_table[static_cast<int64_t>(b) * c.pt_stride + blk];
+    if (phys < 0 || phys >= c.num_pages) return -1;
+  }
+  const int64_t off = static_cast<int64_t>(b) * c.seq_stride + phys * c.block_stride +
+                      static_cast<int64_t>(g) * c.head_stride;
+  if (off < 0 || off + static_cast<int64_t>(min(kBlock, len - blk * kBlock)) * d > c.extent)
+    return -1;
+  return off / d;
+}
+
+// ------------------------------------------------------------------------------- plan
+struct Tile {
+  int b, row0, ntok, pos0, len, steps;
+};
+
+BSA_DEVFN int seq_first(const PackedArgs& a, int b) {
+  return a.cu != nullptr ? a.cu[b] : b * (a.N / a.B);
+}
+BSA_DEVFN int seq_len(const PackedArgs& a, int b) {
+  return a.seq_lens != nullptr ? max(0, min(a.seq_lens[b], a.T)) : a.T;
+}
+
+// Tile `t` of all sequences' tiles, in order; offs[b] is the first tile of sequence b.
+BSA_DEVFN Tile tile_of(const PackedArgs& a, int t) {
+  int lo = 0, hi = a.B - 1;            // the last b with offs[b] <= t
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.offs[mid] <= t) lo = mid; else hi = mid - 1;
+  }
+  const int per = packed_unit_tokens(a.G);
+  const int first = seq_first(a, lo), count = seq_first(a, lo + 1) - first;
+  const int i = (t - a.offs[lo]) * per;
+  Tile r;
+  r.b = lo;
+  r.row0 = first + i;
+  r.ntok = min(per, count - i);
+  r.len = seq_len(a, lo);
+  r.pos0 = r.len - count + i;
+  const int end = a.causal ? max(0, min(r.len, r.pos0 + r.ntok)) : r.len;
+  r.steps = (end + kStep - 1) / kStep;
+  return r;
+}
+
+// One block: lists the units (tile, split of its keys) of one kv head, longest first.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) {
+  __shared__ int warp_sum[32];
+  __shared__ int carry, bad, longest;
+  __shared__ unsigned long long work;
+  __shared__ int bucket[kBuckets];
+  grid_dependency_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = packed_unit_tokens(a.G);
+  if (tid == 0) {
+    carry = 0;
+    bad = 0;
+    longest = 0;
+    work = 0;
+  }
+  for (int i = tid; i < kBuckets; i += kPlanThreads) bucket[i] = 0;
+  __syncthreads();
+  // tiles of each sequence, summed up
+  for (int base = 0; base < a.B; base += kPlanThreads) {
+    const int b = base + tid;
+    int tiles = 0;
+    if (b < a.B) {
+      const int first = seq_first(a, b), last = seq_first(a, b + 1);
+      if (first < 0 || last < first || last > a.N || (b == 0 && first != 0)) {
+        bad = 1;
+      } else {
+        tiles = (last - first + per - 1) / per;
+        const int len = a.seq_lens != nullptr ? a.seq_lens[b] : a.T;
+        if (len < 0 || len > a.T || (a.causal && len < last - first))
+          report(a.status, BSA_DEV_BAD_LENGTH);
+      }
+    }
+    int x = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    int before = carry;
+    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    if (b < a.B) a.offs[b] = before + x - tiles;
+    __syncthreads();
+    if (tid == kPlanThreads - 1) carry = before + x;
+    __syncthreads();
+  }
+  const bool refuse = bad != 0;
+  const int ntiles = refuse ? 0 : carry;
+  if (refuse && tid == 0) report(a.status, BSA_DEV_BAD_LENGTH);
+  // steps of all tiles and of the longest
+  unsigned long long sum = 0;
+  int top = 0;
+  for (int t = tid; t < ntiles; t += kPlanThreads) {
+    const int c = tile_of(a, t).steps;
+    sum += c;
+    top = max(top, c);
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0 && sum > 0) {
+    atomicAdd(&work, sum);
+    atomicMax(&longest, top);
+  }
+  __syncthreads();
+  // Steps a split may have. Without splits the SMs are evenly loaded where the longest unit
+  // is at most half of an SM's share, or where there are several units for each SM and the
+  // longest (started first) is no more than that share. Else about four splits for each SM,
+  // of at least 4 steps, so that the last ones to end are short.
+  const unsigned long long share = (work * a.Hkv + a.num_sms - 1) / a.num_sms;
+  int chunk = 1 << 30;
+  if (a.smax > 1 && !(2ull * longest <= share ||
+                      (static_cast<unsigned long long>(longest) <= share &&
+                       static_cast<long long>(ntiles) * a.Hkv >= 3ll * a.num_sms)))
+    chunk = max(4, static_cast<int>((share + 3) / 4));
+  const int shift = max(0, 32 - __clz(longest) - 9);
+  auto splits_of = [&](int steps) { return max(1, min(a.smax, (steps + chunk - 1) / chunk)); };
+  auto bucket_of = [&](int steps, int n) {
+    return kBuckets - 1 - min(kBuckets - 1, ((steps + n - 1) / n) >> shift);
+  };
+  bool any = false;
+  for (int t = tid; t < ntiles; t += kPlanThreads) {
+    const Tile x = tile_of(a, t);
+    const int n = splits_of(x.steps);
+    any |= n > 1;
+    atomicAdd(&bucket[bucket_of(x.steps, n)], n);
+  }
+  any = __syncthreads_or(any) || a.partial;
+  // exclusive sums of the buckets (kBuckets <= kPlanThreads)
+  int mine = tid < kBuckets ? bucket[tid] : 0, x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sum[warp] = x;
+  __syncthreads();
+  int before = 0;
+  for (int w = 0; w < warp; ++w) before += warp_sum[w];
+  if (tid < kBuckets) bucket[tid] = before + x - mine;
+  if (tid == kPlanThreads - 1) {
+    a.head[0] = before + x;
+    a.head[1] = 0;
+    a.head[2] = any ? 1 : 0;
+  }
+  __syncthreads();
+  for (int t = tid; t < ntiles; t += kPlanThreads) {
+    const Tile y = tile_of(a, t);
+    const int n = splits_of(y.steps);
+    const int at = atomicAdd(&bucket[bucket_of(y.steps, n)], n);
+    for (int s = 0; s < n; ++s) {
+      const int s0 = static_cast<int>(static_cast<int64_t>(y.steps) * s / n);
+      const int s1 = static_cast<int>(static_cast<int64_t>(y.steps) * (s + 1) / n);
+      a.entries[2 * (at + s)] = make_int4(y.b, y.row0, y.ntok, y.pos0);
+      a.entries[2 * (at + s) + 1] = make_int4(y.len, s0, s1, s | (n << 16));
+    }
+    if (any)
+      for (int i = 0; i < y.ntok; ++i) a.row_splits[y.row0 + i] = n;
+  }
+  if (any) {   // rows of no sequence
+    const int end = refuse ? 0 : seq_first(a, a.B);
+    for (int n = end + tid; n < a.N; n += kPlanThreads) a.row_splits[n] = 0;
+  }
+}
+
+// ------------------------------------------------------------------------------- main
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_attn_kernel(const PackedArgs a, const __grid_constant__ CUtensorMap tmq,
+                       const __grid_constant__ CUtensorMap tmk,
+                       const __grid_constant__ CUtensorMap tmv) {
+  using C = Cfg<D>;
+  constexpr int NS = C::kStages;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::kOffBar);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int half_tok = 128 / a.G;      // tokens of one tile
+
+  if (threadIdx.x == 0) {
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&bars->info_full[x], 1);
+      mbar_init(&bars->info_empty[x], 11);   // 2 issuers, the patch warp, 8 softmax warps
+      mbar_init(&bars->q_full[x], 1);
+      mbar_init(&bars->q_empty[x], 1);
+      mbar_init(&bars->s_full[x], 1);
+      mbar_init(&bars->p_ready[x], 4);
+      mbar_init(&bars->o_full[x], 1);
+      mbar_init(&bars->mma_done[x], 1);
+    }
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&bars->kv_full[s], 1);
+      mbar_init(&bars->kv_empty[s], 2);      // both issuers
+      mbar_init(&bars->kv_raw[s], 1);
+    }
+    bars->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) {
+    tc::tmem_alloc(&bars->tmem_base, kTmemCols);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = bars->tmem_base;
+  grid_dependency_wait();
+
+  if (warp < kWarpSm) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == kWarpLoad) {
+      // ---------------------------------------------------------------- Q / K / V
+      const int entries = a.head[0];
+      const int units = entries * a.Hkv;
+      uint32_t un = 0, kc = 0, qc[2] = {0, 0};
+      bool ok = true;
+      while (ok) {
+        const int slot = un & 1;
+        Unit U = {-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+        int u = -1;
+        if (lane == 0) u = atomicAdd(&a.head[1], 1);
+        u = __shfl_sync(0xffffffffu, u, 0);
+        if (u < units) {
+          const int g = u / entries, e = u - g * entries;
+          const int4 e0 = a.entries[2 * e], e1 = a.entries[2 * e + 1];
+          U = {u, e0.x, g, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w & 0xffff, e1.w >> 16, 0};
+          // blocks with a bad page or beyond the cache: found before the unit starts
+          const int nblk = (U.len + kBlock - 1) / kBlock;
+          bool bad = false;
+          for (int blk = 2 * U.step0 + lane; blk < min(2 * U.step1, nblk); blk += 32)
+            bad |= block_row(a.k, U.b, g, blk, U.len, D) < 0 ||
+                   block_row(a.v, U.b, g, blk, U.len, D) < 0;
+          U.bad = __any_sync(0xffffffffu, bad) ? 1 : 0;
+          if (U.bad && lane == 0) report(a.status, BSA_DEV_BAD_PAGE);
+        }
+        if (lane == 0) {
+          if (!mbar_wait_sleep(&bars->info_empty[slot], ((un >> 1) & 1) ^ 1)) {
+            ok = false;
+          } else {
+            bars->info[slot] = U;
+            mbar_arrive(&bars->info_full[slot]);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok || U.u < 0 || aborted(bars)) break;
+        ++un;
+        if (U.step1 <= U.step0) continue;
+        const int ntiles = U.ntok > half_tok ? 2 : 1;
+        if (lane == 0) {
+          for (int t = 0; t < ntiles && ok; ++t) {
+            if (!mbar_wait_sleep(&bars->q_empty[t], (qc[t] & 1) ^ 1)) { ok = false; break; }
+            mbar_arrive_expect_tx(&bars->q_full[t], C::kTile);
+            for (int x = 0; x < C::kHalves; ++x)
+              tma_load_3d(smem + t * C::kTile + x * C::kSlab, &tmq, x * 64, U.g * a.G,
+                          U.row0 + t * half_tok, &bars->q_full[t]);
+            ++qc[t];
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        const int nblk = (U.len + kBlock - 1) / kBlock;
+        for (int s0 = U.step0; s0 < U.step1 && ok; s0 += 16) {
+          // the blocks of 16 steps, one a lane
+          const int blk = 2 * s0 + lane;
+          int rk = -1, rv = -1;
+          if (blk < nblk && blk < 2 * U.step1) {
+            rk = static_cast<int>(block_row(a.k, U.b, U.g, blk, U.len, D));
+            rv = static_cast<int>(block_row(a.v, U.b, U.g, blk, U.len, D));
+            if (rk < 0 || rv < 0) rk = rv = -1;
+          }
+          const int n_here = min(16, U.step1 - s0);
+          for (int q = 0; q < n_here; ++q) {
+            const int k0 = __shfl_sync(0xffffffffu, rk, 2 * q), k1 = __shfl_sync(0xffffffffu, rk, 2 * q + 1);
+            const int v0 = __shfl_sync(0xffffffffu, rv, 2 * q), v1 = __shfl_sync(0xffffffffu, rv, 2 * q + 1);
+            if (lane == 0) {
+              // a step that has the sequence's end or a bad block goes through the patch warp
+              const bool patch = (s0 + q + 1) * kStep > U.len || k0 < 0 || k1 < 0;
+              for (int kv = 0; kv < 2 && ok; ++kv, ++kc) {
+                const int s = kc % NS;
+                if (!mbar_wait_sleep(&bars->kv_empty[s], ((kc / NS) & 1) ^ 1)) { ok = false; break; }
+                uint64_t* bar = kv == 1 && patch ? &bars->kv_raw[s] : &bars->kv_full[s];
+                const int r0 = kv ? v0 : k0, r1 = kv ? v1 : k1;
+                const uint32_t bytes = ((r0 >= 0) + (r1 >= 0)) * (C::kTile / 2);
+                if (bytes > 0) mbar_arrive_expect_tx(bar, bytes); else mbar_arrive(bar);
+                unsigned char* st = smem + C::kOffKV + s * C::kTile;
+                const CUtensorMap* map = kv ? &tmv : &tmk;
+                for (int x = 0; x < C::kHalves; ++x) {
+                  if (r0 >= 0) tma_load_2d(st + x * C::kSlab, map, x * 64, r0, bar);
+                  if (r1 >= 0) tma_load_2d(st + x * C::kSlab + 8192, map, x * 64, r1, bar);
+                }
+              }
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        }
+      }
+      if (lane == 0 && !ok) {
+        set_abort(bars, a.status);
+        // copies in flight must land before the block exits (bounded)
+        for (uint32_t k = (kc > NS ? kc - NS : 0); k < kc; ++k)
+          mbar_wait_sleep(&bars->kv_full[k % NS], (k / NS) & 1, 100000000ull);
+        for (int t = 0; t < 2; ++t)
+          if (qc[t] > 0) mbar_wait_sleep(&bars->q_full[t], (qc[t] - 1) & 1, 100000000ull);
+      }
+    } else if (warp == kWarpPatch) {
+      // -------------------------- V rows behind the end (or of a bad block) become zero
+      uint32_t un = 0, kc = 0, raw_phase = 0;
+      while (true) {
+        const int slot = un & 1;
+        if (!warp_wait_sleep(&bars->info_full[slot], (un >> 1) & 1)) {
+          if (lane == 0) set_abort(bars, a.status);
+          break;
+        }
+        const Unit U = bars->info[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->info_empty[slot]);
+        ++un;
+        if (U.u < 0 || aborted(bars)) break;
+        const int n = U.step1 - U.step0;
+        // without bad blocks only the last step can have the end
+        bool ok = true;
+        for (int j = U.bad ? 0 : max(0, n - 1); j < n && ok; ++j) {
+          const int step = U.step0 + j, nblk = (U.len + kBlock - 1) / kBlock;
+          int keep[2];                 // rows of each block that stay
+          bool patch = (step + 1) * kStep > U.len;
+          for (int i = 0; i < 2; ++i) {
+            const int blk = 2 * step + i;
+            keep[i] = max(0, min(kBlock, U.len - blk * kBlock));
+            if (U.bad && blk < nblk && (block_row(a.k, U.b, U.g, blk, U.len, D) < 0 ||
+                                        block_row(a.v, U.b, U.g, blk, U.len, D) < 0)) {
+              keep[i] = 0;
+              patch = true;
+            }
+          }
+          if (!patch) continue;
+          const int s = (kc + 2 * j + 1) % NS;
+          if (!warp_wait_sleep(&bars->kv_raw[s], (raw_phase >> s) & 1)) { ok = false; break; }
+          raw_phase ^= 1u << s;
+          unsigned char* st = smem + C::kOffKV + s * C::kTile;
+          for (int x = 0; x < C::kHalves; ++x)
+            for (int i = 0; i < 2; ++i)
+              for (int c = keep[i] * 8 + lane; c < kBlock * 8; c += 32)
+                *reinterpret_cast<uint4*>(st + x * C::kSlab + i * 8192 + c * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->kv_full[s]);
+        }
+        if (!ok) {
+          if (lane == 0) set_abort(bars, a.status);
+          break;
+        }
+        kc += 2 * max(0, n);
+      }
+    } else if (lane == 0) {
+      // ------------------------------------------------------ MMA issuer of tile t
+      const int t = warp - kWarpMma;
+      const uint32_t idS = tc::idesc_f16(128, kStep, 1, false);
+      const uint32_t idPV = tc::idesc_f16(128, D, 1, true);
+      const uint32_t sbase = smem_u32(smem);
+      const uint64_t dq = tc::smem_desc_sw128(sbase + t * C::kTile, 16, 1024);
+      const uint32_t s_tm = tmem + 256 + 128 * t, o_tm = tmem + 128 * t;
+      uint32_t un = 0, kc = 0, qc = 0, pc = 0;
+      bool ok = true;
+      auto full = [&](uint32_t k) { return mbar_wait_sleep(&bars->kv_full[k % NS], (k / NS) & 1); };
+      auto scores = [&](uint32_t k) {
+        const uint64_t dk = tc::smem_desc_sw128(sbase + C::kOffKV + (k % NS) * C::kTile, 16, 1024);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint64_t off = ((ks >> 2) * C::kSlab + (ks & 3) * 32) >> 4;
+          tc::mma_ss(s_tm, dq + off, dk + off, idS, ks > 0);
+        }
+        tc::commit(&bars->s_full[t]);
+        tc::commit(&bars->kv_empty[k % NS]);
+      };
+      while (ok) {
+        const int slot = un & 1;
+        if (!mbar_wait_sleep(&bars->info_full[slot], (un >> 1) & 1)) { ok = false; break; }
+        const Unit U = bars->info[slot];
+        mbar_arrive(&bars->info_empty[slot]);
+        ++un;
+        if (U.u < 0 || aborted(bars)) break;
+        const int n = U.step1 - U.step0;
+        if (n <= 0) continue;
+        if (t == 1 && U.ntok <= half_tok) {
+          // no rows: the stages are free as far as this tile goes
+          for (int j = 0; j < 2 * n && ok; ++j, ++kc) {
+            ok = full(kc);
+            if (ok) mbar_arrive(&bars->kv_empty[kc % NS]);
+          }
+          continue;
+        }
+        if (!mbar_wait_sleep(&bars->q_full[t], qc & 1)) { ok = false; break; }
+        ++qc;
+        if (!full(kc)) { ok = false; break; }
+        tc::fence_after_sync();
+        scores(kc);
+        if (n == 1) tc::commit(&bars->q_empty[t]);
+        for (int j = 0; j < n; ++j) {
+          const uint32_t kv = kc + 2 * j + 1;   // the stage of V (j); K (j + 1) is the next one
+          if (!mbar_wait_sleep(&bars->p_ready[t], pc & 1)) { ok = false; break; }
+          ++pc;
+          if (!full(kv)) { ok = false; break; }
+          tc::fence_after_sync();
+          const uint64_t dv =
+              tc::smem_desc_sw128(sbase + C::kOffKV + (kv % NS) * C::kTile, C::kSlab, 1024);
+#pragma unroll
+          for (int kk = 0; kk < kStep / 16; ++kk)
+            tc::mma_ts(o_tm, s_tm + kk * 8, dv + ((kk * 2048) >> 4), idPV, j > 0 || kk > 0);
+          tc::commit(&bars->kv_empty[kv % NS]);
+          if (j + 1 < n) {
+            if (!full(kv + 1)) { ok = false; break; }
+            tc::fence_after_sync();
+            scores(kv + 1);
+            if (j + 2 == n) tc::commit(&bars->q_empty[t]);   // Q is free after the last scores
+          } else {
+            tc::commit(&bars->o_full[t]);
+          }
+        }
+        kc += 2 * n;
+      }
+      if (!ok) set_abort(bars, a.status);
+      // every MMA this thread issued must finish before tensor memory is freed (bounded)
+      tc::commit(&bars->mma_done[t]);
+      mbar_wait_sleep(&bars->mma_done[t], 0, 200000000ull);
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax of tile t
+    // Warp w has the tile's rows 32 (w % 4) .. + 31 (its quarter of tensor memory), one a
+    // thread.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int t = (warp - kWarpSm) >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_col = tmem + lane_addr + 256 + 128 * t;
+    const uint32_t o_col = tmem + lane_addr + 128 * t;
+    const int tok = t * half_tok + row / a.G, hh = row % a.G;
+    const int warp_tok = t * half_tok + ((warp & 3) * 32) / a.G;   // of the warp's first row
+    const float sc = a.scale_log2;
+    uint32_t un = 0, stepc = 0, oc = 0;
+    while (true) {
+      const int slot = un & 1;
+      if (!warp_wait(&bars->info_full[slot], (un >> 1) & 1)) {
+        if (lane == 0) set_abort(bars, a.status);
+        break;
+      }
+      const Unit U = bars->info[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->info_empty[slot]);
+      ++un;
+      if (U.u < 0 || aborted(bars)) break;
+      if (t == 1 && U.ntok <= half_tok) continue;
+      const bool live = tok < U.ntok;
+      // the last key this row sees
+      const int last = !live ? -1 : a.causal ? min(U.pos0 + tok, U.len - 1) : U.len - 1;
+      float m = -INFINITY;
+      float2 l = make_float2(0.f, 0.f);
+      bool ok = true;
+      const bool idle = warp_tok >= U.ntok;   // no row of this warp exists
+      for (int step = U.step0; step < U.step1; ++step, ++stepc) {
+        if (!warp_wait(&bars->s_full[t], stepc & 1)) { ok = false; break; }
+        if (idle) {   // rows of P that nobody reads
+          if (lane == 0) mbar_arrive(&bars->p_ready[t]);
+          continue;
+        }
+        tc::fence_after_sync();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tc::ld32(s_col + 32 * i, s[i]);
+        tc::wait_ld();
+        const int lim = last - step * kStep;   // columns 0 .. lim are visible
+        if (lim < kStep - 1) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (32 * i + c > lim) s[i][c] = 0xff800000u;
+        }
+        if (U.bad) {
+          for (int x = 0; x < 2; ++x) {
+            const int blk = 2 * step + x;
+            if (blk * kBlock < U.len && (block_row(a.k, U.b, U.g, blk, U.len, D) < 0 ||
+                                         block_row(a.v, U.b, U.g, blk, U.len, D) < 0)) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if ((i >> 1) == x) s[i][c] = 0xff800000u;
+            }
+          }
+        }
+        float mx[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          mx[i] = max3(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]), __uint_as_float(s[i][2]));
+#pragma unroll
+          for (int c = 3; c < 31; c += 2)
+            mx[i] = max3(mx[i], __uint_as_float(s[i][c]), __uint_as_float(s[i][c + 1]));
+          mx[i] = fmaxf(mx[i], __uint_as_float(s[i][31]));
+        }
+        const float x = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+        const bool up = x > m + 8.0f;
+        const float f = up ? ex2(m - x) : 1.0f;
+        if (__any_sync(0xffffffffu, up)) {
+          if (up) {
+            l.x *= f;
+            l.y *= f;
+            m = x;
+          }
+          if (step > U.step0) {
+            // the tile's P V of the last step is done (its S was issued behind it)
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t ov[32];
+              tc::ld32(o_col + c, ov);
+              tc::wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f);
+              tc::st32(o_col + c, ov);
+            }
+          }
+        }
+        const float neg = m == -INFINITY ? 0.f : -m;
+        const float2 neg2 = make_float2(neg, neg), sc2 = make_float2(sc, sc);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float2 v = __ffma2_rn(
+                make_float2(__uint_as_float(s[i][c]), __uint_as_float(s[i][c + 1])), sc2, neg2);
+            const float2 p = make_float2(ex2(v.x), ex2(v.y));
+            l = __fadd2_rn(l, p);
+            s[i >> 1][(i & 1) * 16 + c / 2] = pack_bf16(p.x, p.y);
+          }
+        }
+        tc::st32(s_col, s[0]);
+        tc::st32(s_col + 32, s[1]);
+        tc::wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_ready[t]);
+      }
+      if (!ok || aborted(bars)) {
+        if (lane == 0) set_abort(bars, a.status);
+        break;
+      }
+      // ---- epilogue
+      const bool empty = U.step1 <= U.step0;
+      if (!empty) {
+        if (!warp_wait(&bars->o_full[t], oc & 1)) {
+          if (lane == 0) set_abort(bars, a.status);
+          break;
+        }
+        ++oc;
+        tc::fence_after_sync();
+      }
+      const float L = l.x + l.y;
+      const bool part = U.nsplit > 1 || a.partial;
+      const float inv = part ? 1.0f : L == 0.f ? 0.f : 1.0f / L;
+      const int64_t at = (static_cast<int64_t>(U.row0) + tok) * a.Hq + U.g * a.G + hh;
+      const int64_t pat = static_cast<int64_t>(U.split) * a.N * a.Hq + at;
+      if (!idle) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t ov[32];
+          if (empty) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ov[i] = 0u;
+          } else {
+            tc::ld32(o_col + c, ov);
+            tc::wait_ld();
+          }
+          if (live) {
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(ov[i]) * inv;
+            if (!part) {
+              uint4* ob = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + at * D + c);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                ob[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                                   pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+            }
+            float* of = part ? a.part_o + pat * D + c : a.o_f32 != nullptr ? a.o_f32 + at * D + c : nullptr;
+            if (of != nullptr) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                reinterpret_cast<float4*>(of)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            }
+          }
+        }
+        if (live) {
+          if (part)
+            *reinterpret_cast<float2*>(a.part_ml + 2 * pat) = make_float2(m, L);
+          else
+            a.lse[at] = L == 0.f ? -INFINITY : (m + log2f(L)) * kLn2;
+        }
+      }
+      tc::fence_before_sync();
+    }
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------------------- merge
+// One warp per (row, head): joins the splits' (o, m, l) and, with o_own, what the row's own
+// tokens gave.
+template <int D>
+__global__ void __launch_bounds__(256) packed_merge_kernel(const PackedArgs a) {
+  grid_dependency_wait();
+  if (a.head[2] == 0) return;
+  constexpr int kPer = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t at = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  if (at >= static_cast<int64_t>(a.N) * a.Hq) return;
+  const int n = a.row_splits[at / a.Hq];
+  if (n == 0 || (n == 1 && !a.partial)) return;
+  const int64_t rows = static_cast<int64_t>(a.N) * a.Hq;
+  const float own = a.lse_own != nullptr ? a.lse_own[at] * kLog2e : -INFINITY;
+  float M = own;
+  for (int s = lane; s < n; s += 32) M = fmaxf(M, a.part_ml[2 * (s * rows + at)]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float base = M == -INFINITY ? 0.f : M;
+  float L = 0.f;
+  float2 o[kPer / 2];
+#pragma unroll
+  for (int q = 0; q < kPer / 2; ++q) o[q] = make_float2(0.f, 0.f);
+  for (int c = 0; c < n; c += 32) {
+    float f = 0.f;
+    if (c + lane < n) {
+      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * ((c + lane) * rows + at));
+      f = ex2(ml.x - base);
+      L += ml.y * f;
+    }
+    const int here = min(32, n - c);
+#pragma unroll 4
+    for (int j = 0; j < here; ++j) {
+      const float fj = __shfl_sync(0xffffffffu, f, j);
+      const float2* po = reinterpret_cast<const float2*>(a.part_o + ((c + j) * rows + at) * D);
+#pragma unroll
+      for (int q = 0; q < kPer / 2; ++q) {
+        const float2 v = po[lane + 32 * q];
+        o[q].x = fmaf(v.x, fj, o[q].x);
+        o[q].y = fmaf(v.y, fj, o[q].y);
+      }
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+  if (own != -INFINITY) {     // o_own is normalised: a part with l = 1 at its log-sum
+    const float f = ex2(own - base);
+    L += f;
+    const float2* po = reinterpret_cast<const float2*>(a.o_own + at * D);
+#pragma unroll
+    for (int q = 0; q < kPer / 2; ++q) {
+      const float2 v = po[lane + 32 * q];
+      o[q].x = fmaf(v.x, f, o[q].x);
+      o[q].y = fmaf(v.y, f, o[q].y);
+    }
+  }
+  const float inv = L == 0.f ? 0.f : 1.0f / L;
+#pragma unroll
+  for (int q = 0; q < kPer / 2; ++q) {
+    const float2 v = make_float2(o[q].x * inv, o[q].y * inv);
+    reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.o) + at * D)[lane + 32 * q] = pack_bf16(v.x, v.y);
+    if (a.o_f32 != nullptr) reinterpret_cast<float2*>(a.o_f32 + at * D)[lane + 32 * q] = v;
+  }
+  if (lane == 0) a.lse[at] = L == 0.f ? -INFINITY : (base + log2f(L)) * kLn2;
+}
+
+template <int D>
+cudaError_t launch_d(const PackedArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
+                     const CUtensorMap& tv, int num_sms, cudaStream_t s) {
+  cudaError_t e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a);
+  if (e != cudaSuccess) return e;
+  constexpr int smem = smem_bytes<D>();
+  auto kern = packed_attn_kernel<D>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t units = static_cast<int64_t>(a.max_entries) * a.Hkv;
+  const int grid = static_cast<int>(units < num_sms ? units : num_sms);
+  e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s, a, tq, tk, tv);
+  if (e != cudaSuccess || (a.smax == 1 && !a.partial)) return e;
+  const int64_t warps = static_cast<int64_t>(a.N) * a.Hq;
+  return launch_pdl(packed_merge_kernel<D>, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_packed(const PackedArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
+                          const CUtensorMap& tv, int num_sms, cudaStream_t s) {
+  return a.d == 128 ? launch_d<128>(a, tq, tk, tv, num_sms, s) : launch_d<64>(a, tq, tk, tv, num_sms, s);
+}
+
+}  // namespace bsa

@@ -63,11 +63,13 @@ typedef enum {
 #define BSA_DEV_TIMEOUT 0x8    /* a bounded wait inside a kernel gave up; outputs invalid */
 #define BSA_DEV_FP16_RANGE 0x10 /* a value outside the fp16 range: a prefill V value, or an
                                    index query scored against an FP4 index-key cache */
+#define BSA_DEV_BAD_LENGTH 0x20 /* cu_seqlens not ascending inside [0, N], a length outside
+                                   [0, T], or a sequence shorter than its new rows */
 
 typedef enum { BSA_PHASE_DECODE = 0, BSA_PHASE_PREFILL = 1 } bsa_phase_t;
 
 typedef enum { BSA_OP_SCORE = 0, BSA_OP_SELECT = 1, BSA_OP_DECODE = 2, BSA_OP_PREFILL = 3,
-               BSA_OP_PBS_PERMUTE = 4 } bsa_op_t;
+               BSA_OP_PBS_PERMUTE = 4, BSA_OP_ATTEND_PACKED = 5, BSA_OP_DECODE_SHARED = 6 } bsa_op_t;
 
 /* Addressing of one bf16 cache tensor (K, V or index keys), contiguous or paged.
  * Token t of sequence b, kv head g starts at element
@@ -274,6 +276,107 @@ bsa_status_t bsa_quantize_index_keys(const bsa_problem_t* prob, bsa_cache_t k_id
  * Prefill problems return BSA_ERR_UNSUPPORTED. */
 bsa_status_t bsa_score_blocks_q(const bsa_problem_t* prob, const void* q_idx, bsa_qcache_t k_idx,
                                 float* block_scores, int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * New tokens: head norms with rotary positions, appending to the caches, dense
+ * attention over packed rows, and decode over a shared prefix. These calls fill the
+ * caches that the calls above read, and attend where block sparsity saves nothing
+ * (short prompts, chunks of prompts, prefixes that a whole batch reads).
+ *
+ * Token rows. N rows lie packed: sequence b has the rows [cu_seqlens[b],
+ * cu_seqlens[b+1]), in order, and its last row is its newest token, so that row i of
+ * sequence b is token seq_lens[b] - (cu_seqlens[b+1] - i) of it. Rows behind
+ * cu_seqlens[B] are padding: nothing of theirs is read or written. Lengths live on
+ * the device, so a captured graph serves changing lengths.
+ * ---------------------------------------------------------------------- */
+typedef enum { BSA_TYPE_BF16 = 0, BSA_TYPE_F16 = 1, BSA_TYPE_F32 = 2 } bsa_type_t;
+
+/* Head rows in memory: element c of head h of row n is element
+ * n*token_stride + h*head_stride + c from `base`; the elements of one head are
+ * contiguous and start on a 16-byte boundary (base and strides). base = NULL: none. */
+typedef struct {
+  void* base;
+  int64_t token_stride;      /* elements */
+  int64_t head_stride;       /* elements */
+  int32_t type;              /* bsa_type_t */
+} bsa_rows_t;
+
+typedef struct {
+  int32_t N;                 /* token rows, padding included (0: nothing to do) */
+  int32_t B;                 /* sequences (bsa_decode_shared: prefixes) */
+  int32_t Hq, Hkv, d, r, block;
+  int32_t T;                 /* capacity: every seq_lens[b] <= T */
+  const int32_t* cu_seqlens; /* device [B+1], or NULL: N/B rows each (N % B == 0) */
+  const int32_t* seq_lens;   /* device [B]: tokens of each sequence, its rows included;
+                                NULL = T */
+  const int32_t* positions;  /* device [N]: position each row is rotated to, or NULL: its
+                                token number in its sequence. Cache slots always go by
+                                the token number. */
+  const uint64_t* rope_steps;/* device [rope_dim / 2]: what pair i turns by per position, in
+                                units of 2^-64 turns (frequency / (2 pi) * 2^64 mod 2^64) */
+  int32_t rope_dim;          /* leading elements of each head that are rotated: 0 (none) or a
+                                multiple of 16 up to d */
+  int32_t rope_interleaved;  /* pair i is elements (i, i + rope_dim/2), or with 1 (2i, 2i+1) */
+  float rope_factor;         /* multiplies cos and sin; 0 = 1 */
+  int32_t norm;              /* 1: root-mean-square norm of each q and k head first */
+  float eps;                 /* added to the mean square (norm = 1) */
+  const float* q_weight;     /* device [d] or NULL = ones (norm = 1) */
+  const float* k_weight;     /* device [d] or NULL = ones (norm = 1) */
+  int32_t causal;            /* bsa_attend_packed: 1: a row sees the tokens up to itself;
+                                0: it sees its whole sequence */
+  float attn_scale;          /* softmax scale; 0 = 1/sqrt(d) */
+  int64_t q_stride;          /* attention: elements between the query rows of two tokens
+                                (a multiple of 8); 0 = Hq*d */
+} bsa_tokens_t;
+
+/* Head norm and rotary positions. For each row and each head of q and k (width d):
+ *   y = x * w / sqrt(mean(x^2) + eps)            (norm = 1; else y = x)
+ *   (y_a, y_b) -> factor * (y_a cos - y_b sin, y_b cos + y_a sin)   for each pair
+ * at angle position * step. The angle is an integer product modulo 2^64, so it is
+ * exact to 2^-32 turns at every position; everything else is float32, rounded once to
+ * the bf16 output. q [N, Hq, d] -> q_out, k [N, Hkv, d] -> k_out (bf16); q or k may
+ * have base = NULL. An output may be its own input (same base, strides and type). */
+bsa_status_t bsa_norm_rope(const bsa_tokens_t* tok, bsa_rows_t q, bsa_rows_t q_out, bsa_rows_t k,
+                           bsa_rows_t k_out, int32_t* dev_status, void* stream);
+
+/* Append rows to the caches: k (normed and rotated as above), v and, where kidx.base
+ * is not NULL, the index keys kidx [N, Hkv, r], each rounded to bf16, into their
+ * token's slot of k_cache, v_cache and kidx_cache. Where q.base is not NULL its heads
+ * are normed and rotated into q_out by the same launch. A row whose slot does not
+ * exist (bad page, outside the extent) is not written and reported. Two rows with
+ * the same slot (a page that two sequences share) leave either's values. */
+bsa_status_t bsa_append_kv(const bsa_tokens_t* tok, bsa_rows_t k, bsa_rows_t v, bsa_rows_t kidx,
+                           bsa_cache_t k_cache, bsa_cache_t v_cache, bsa_cache_t kidx_cache,
+                           bsa_rows_t q, bsa_rows_t q_out, int32_t* dev_status, void* stream);
+
+/* Dense attention of packed rows over their sequences' caches, causal or not: row i of
+ * sequence b sees its tokens 0 .. token(i) (causal) or 0 .. seq_lens[b]-1.
+ * q [N, Hq, d] bf16 (tok->q_stride); k, v caches (width d).
+ * Outputs: o [N, Hq, d] bf16, lse [N, Hq] fp32 (natural log; -inf and o = 0 where a
+ * row sees nothing), o_f32 [N, Hq, d] fp32 or NULL. K and V of a sequence's own tokens
+ * have to be finite; what lies behind them in the last page may be anything. A block
+ * with a bad page is left out and reported. Where cu_seqlens is bad nothing is written.
+ * Workspace: bsa_packed_workspace_size. */
+bsa_status_t bsa_attend_packed(const bsa_tokens_t* tok, const void* q, bsa_cache_t k,
+                               bsa_cache_t v, void* o, float* lse, float* o_f32, void* workspace,
+                               size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* Decode attention for sequences that share prefixes, each prefix read once for all its
+ * sequences. Here `B` counts prefixes: rows [cu_seqlens[p], cu_seqlens[p+1]) are one
+ * query token each of the sequences behind prefix p, which has seq_lens[p] tokens in the
+ * caches k and v (whose sequence index is p); every row sees its whole prefix.
+ * o_own [N, Hq, d] fp32 and lse_own [N, Hq] fp32 are the attention over each sequence's
+ * own tokens (bsa_decode's o_f32 and lse; lse_own = -inf: none), or both NULL. The
+ * outputs are the attention over prefix and own tokens together:
+ *   lse = log(e^lse_p + e^lse_own),  o = e^(lse_p - lse) o_p + e^(lse_own - lse) o_own.
+ * o, lse and o_f32 as in bsa_attend_packed; o_f32 may be o_own and lse may be lse_own. */
+bsa_status_t bsa_decode_shared(const bsa_tokens_t* tok, const void* q, bsa_cache_t k,
+                               bsa_cache_t v, const float* o_own, const float* lse_own, void* o,
+                               float* lse, float* o_f32, void* workspace, size_t workspace_bytes,
+                               int32_t* dev_status, void* stream);
+
+/* Workspace bytes `op` (BSA_OP_ATTEND_PACKED or BSA_OP_DECODE_SHARED) needs. Host only. */
+bsa_status_t bsa_packed_workspace_size(const bsa_tokens_t* tok, int32_t op, size_t* bytes);
 
 /* Size of the fixed device scratch array used by bsa_decode_noalloc (8 MiB). */
 #define BSA_NOALLOC_SCRATCH_BYTES (8u << 20)

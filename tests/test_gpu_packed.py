@@ -1,0 +1,446 @@
+"""Dense packed attention and shared-prefix decode on the GPU against 64 bits.
+
+Tolerances. With s the largest scale * sum |q_c k_c| of a row: a score is a sum of d products
+of bf16 values (exact in fp32) with one rounding of at most 2^-23 (of what it adds up) each,
+so it is off by at most e = d 2^-23 s; the base-2 exponential adds 2^-17. P is rounded to bf16
+(2^-8 relative), O adds n products with 2^-23 each. So |o - o_exact| is at most
+(2^-8 + 2 (e + 2^-17) + n 2^-23) sum_j p_j |v_j| before it is rounded to bf16 (2^-8 |o|), and
+lse is off by at most e + 2^-17 + n 2^-24 + 2^-22 |lse|."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_long_06_b200 as bsa
+from oracle import tokens_oracle as TO
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+
+
+def f64(t):
+    return t.detach().to("cpu", torch.float64).numpy()
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def randn(*shape, seed=0, scale=1.0):
+    return (torch.randn(*shape, generator=gen(seed), device="cuda") * scale).to(torch.bfloat16)
+
+
+class Paged:
+    """Pools with scattered pages; every slot behind a sequence's end holds NaN or infinity."""
+
+    def __init__(self, lens, Hkv, d, seed, spare=3, T=None):
+        nb = [-(-n // 64) for n in lens]
+        width = max(1, max(nb) if T is None else -(-T // 64))
+        P = sum(nb) + spare
+        self.K, self.V = (randn(P, Hkv, 64, d, seed=seed + i) for i in (0, 1))
+        order = torch.randperm(P, generator=torch.Generator().manual_seed(seed))
+        self.pt = torch.full((len(lens), width), -1, dtype=torch.int32)
+        at = 0
+        for b, n in enumerate(nb):
+            self.pt[b, :n] = order[at:at + n]
+            at += n
+        for p in order[at:].tolist():
+            self.K[p], self.V[p] = float("nan"), float("inf")
+        for b, n in enumerate(lens):
+            if n % 64:
+                p = int(self.pt[b, nb[b] - 1])
+                self.K[p, :, n % 64:], self.V[p, :, n % 64:] = float("nan"), float("-inf")
+        self.pt = self.pt.cuda()
+        self.lens, self.T = lens, 64 * width if T is None else T
+
+    def caches(self):
+        return bsa.paged_cache(self.K, self.pt), bsa.paged_cache(self.V, self.pt)
+
+    def keys(self, X, b, n):
+        """[Hkv, n, d] of sequence b, in 64 bits."""
+        pages = self.pt[b, :-(-n // 64)].long()
+        return f64(X[pages]).transpose(1, 0, 2, 3).reshape(X.shape[1], -1, X.shape[3])[:, :n]
+
+
+def exact(q, mem, cu, lens, causal, G, scale=None, hide=None):
+    """(o, lse, spread, size, n) over all rows; rows of no sequence keep lse = nan."""
+    N, Hq, d = q.shape
+    scale = 1 / math.sqrt(d) if scale is None else scale
+    o, spread = np.zeros((N, Hq, d)), np.zeros((N, Hq, d))
+    lse, size = np.full((N, Hq), np.nan), np.zeros((N, Hq))
+    qq = f64(q)
+    for b, n in enumerate(lens):
+        r = slice(cu[b], cu[b + 1])
+        c = cu[b + 1] - cu[b]
+        K, V = mem.keys(mem.K, b, n), mem.keys(mem.V, b, n)
+        vis = np.ones((c, n), bool)
+        if causal:
+            vis = np.arange(n)[None, :] <= (n - c + np.arange(c))[:, None]
+        if hide is not None:
+            vis = vis & ~hide(b, np.arange(n))[None, :]
+        for h in range(Hq):
+            o[r, h], lse[r, h], spread[r, h], size[r, h] = TO.attend_rows(
+                qq[r, h], K[h // G], V[h // G], scale, vis)
+    return o, lse, spread, size
+
+
+def check(step, want, keys, d):
+    o, lse, spread, size = want
+    live = ~np.isnan(lse)
+    e = d * 2.0 ** -23 * size + 2.0 ** -17
+    got32, got, gl = f64(step.o_f32), f64(step.o), f64(step.lse)
+    bound = (2.0 ** -8 + 2 * e + keys * 2.0 ** -23)[..., None] * spread
+    off = np.abs(got32 - o)
+    assert np.isfinite(got32[live]).all()
+    assert (off <= bound)[live].all(), float((off - bound)[live].max())
+    assert torch.equal(step.o_f32.to(torch.bfloat16)[torch.from_numpy(live)], step.o[torch.from_numpy(live)])
+    none = live & np.isinf(lse)
+    assert (gl[none] == -np.inf).all() and not got[none].any()
+    some = live & np.isfinite(lse)
+    off = np.abs(gl[some] - lse[some])
+    bound = (e + keys * 2.0 ** -24)[some] + 2.0 ** -22 * np.abs(lse[some])
+    assert (off <= bound).all(), float((off - bound).max())
+
+
+def sums(x):
+    return [0] + list(np.cumsum(x))
+
+
+def run_attend(q, mem, cu, lens, Hkv, causal=True, pad=0, status=0, **kw):
+    N, Hq, d = q.shape
+    tok = bsa.Tokens(N=N, B=len(lens), Hq=Hq, Hkv=Hkv, d=d, T=mem.T, cu_seqlens=ints(cu),
+                     seq_lens=ints(lens), causal=causal, **kw)
+    step = bsa.PackedAttention(tok)
+    for x in (step.o, step.lse, step.o_f32):
+        x.fill_(77.0)
+    step.run(q, *mem.caches())
+    assert int(step.status.item()) == status
+    for x in (step.o, step.lse, step.o_f32):
+        assert (x[cu[-1]:] == 77.0).all()       # padding rows
+    return step
+
+
+# ------------------------------------------------------------------ packed attention
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 2, 4, 8, 16])
+@pytest.mark.parametrize("causal", [True, False])
+def test_ragged_batch(d, G, causal):
+    """Prompts, chunks behind a cache, single tokens, a sequence without rows, page and tile
+    ends inside sequences, garbage behind every end."""
+    Hkv = 2
+    new, lens = [1, 70, 0, 257, 1, 33], [1, 70, 5, 300, 515, 129]
+    cu = sums(new)
+    mem = Paged(lens, Hkv, d, seed=G + d)
+    q = randn(cu[-1] + 3, Hkv * G, d, seed=9, scale=1.5)
+    step = run_attend(q, mem, cu, lens, Hkv, causal)
+    check(step, exact(q, mem, cu, lens, causal, G), 515, d)
+
+
+@pytest.mark.parametrize("n", [1, 2, 63, 64, 65, 127, 128, 129, 255, 256, 257, 640])
+def test_prompt_lengths(n):
+    d, G, Hkv = 128, 4, 1
+    mem = Paged([n], Hkv, d, seed=n)
+    q = randn(n, G, d, seed=n + 1, scale=1.5)
+    step = run_attend(q, mem, [0, n], [n], Hkv)
+    check(step, exact(q, mem, [0, n], [n], True, G), n, d)
+
+
+@pytest.mark.parametrize("lens", [[4097], [1, 3000, 64, 0, 128, 5000]])
+def test_single_tokens_split_over_keys(lens):
+    """One row a sequence (an empty sequence has a row too: it sees nothing)."""
+    d, G, Hkv = 128, 4, 2
+    B = len(lens)
+    mem = Paged(lens, Hkv, d, seed=21)
+    q = randn(B, Hkv * G, d, seed=22, scale=2.0)
+    bad = bsa.BSA_DEV_BAD_LENGTH if 0 in lens else 0     # no token, but a row
+    step = run_attend(q, mem, list(range(B + 1)), lens, Hkv, status=bad)
+    check(step, exact(q, mem, list(range(B + 1)), lens, True, G), max(lens), d)
+    # the same rows without cu_seqlens
+    tok = bsa.Tokens(N=B, B=B, Hq=Hkv * G, Hkv=Hkv, d=d, T=mem.T, seq_lens=ints(lens))
+    again = bsa.PackedAttention(tok)
+    again.run(q, *mem.caches())
+    assert torch.equal(again.o, step.o) and torch.equal(again.lse, step.lse)
+
+
+def test_growing_scores_move_the_maximum():
+    """Each block of keys has larger scores than the ones before, so O is rescaled many times;
+    one key late in the row takes nearly all the weight."""
+    d, G, Hkv, n = 128, 2, 1, 700
+    mem = Paged([n], Hkv, d, seed=30)
+    q = randn(40, G, d, seed=31)
+    mean = q.float().mean((0, 1))
+    mean /= mean.norm()
+    for i in range(n):
+        p, r = int(mem.pt[0, i // 64]), i % 64
+        mem.K[p, 0, r] = (mean * (i / 8.0)).to(torch.bfloat16)
+    q = (q.float() + mean * 6.0).to(torch.bfloat16)
+    step = run_attend(q, mem, [0, 40], [n], Hkv)
+    want = exact(q, mem, [0, 40], [n], True, G)
+    assert (want[1].max() > 40)
+    check(step, want, n, d)
+
+
+def test_contiguous_caches_strided_queries_and_scale():
+    d, G, Hkv, B, T = 64, 4, 2, 3, 150
+    lens, new = [150, 77, 3], [20, 77, 1]
+    cu = sums(new)
+    K, V = randn(B, Hkv, T, d, seed=40), randn(B, Hkv, T, d, seed=41)
+    qkv = randn(cu[-1], Hkv * (G + 2), d, seed=42)
+    q = qkv[:, :Hkv * G]
+    tok = bsa.Tokens(N=cu[-1], B=B, Hq=Hkv * G, Hkv=Hkv, d=d, T=T, cu_seqlens=ints(cu),
+                     seq_lens=ints(lens), attn_scale=0.3)
+    step = bsa.PackedAttention(tok)
+    step.run(q, bsa.contiguous_cache(K), bsa.contiguous_cache(V))
+    assert int(step.status.item()) == 0
+
+    class Flat:
+        pass
+    mem = Flat()
+    mem.K, mem.V = K, V
+    mem.keys = lambda X, b, n: f64(X[b, :, :n])
+    check(step, exact(q, mem, cu, lens, True, G, scale=0.3), 150, d)
+
+
+def test_equal_rows_without_lengths():
+    """No cu_seqlens and no seq_lens: B sequences of T tokens, all of them rows."""
+    d, Hkv, G, B, T = 64, 1, 8, 2, 200
+    mem = Paged([T] * B, Hkv, d, seed=43, T=T)
+    q = randn(B * T, G, d, seed=44)
+    tok = bsa.Tokens(N=B * T, B=B, Hq=G, Hkv=Hkv, d=d, T=T)
+    step = bsa.PackedAttention(tok)
+    step.run(q, *mem.caches())
+    check(step, exact(q, mem, [0, T, 2 * T], [T, T], True, G), T, d)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_bad_pages_are_left_out(causal):
+    d, G, Hkv = 128, 4, 2
+    lens, new = [500, 300], [100, 1]
+    cu = sums(new)
+    mem = Paged(lens, Hkv, d, seed=50)
+    q = randn(cu[-1], Hkv * G, d, seed=51)
+    good = mem.pt.clone()
+    mem.pt[0, 2], mem.pt[0, 7], mem.pt[1, 0] = -5, 10 ** 6, 1 << 30
+    step = run_attend(q, mem, cu, lens, Hkv, causal, status=bsa.BSA_DEV_BAD_PAGE)
+    mem.pt = good
+    hide = lambda b, j: np.isin(j // 64, [2, 7] if b == 0 else [0])
+    check(step, exact(q, mem, cu, lens, causal, G, hide=hide), 500, d)
+
+
+def test_bad_lengths_write_nothing_or_clamp():
+    d, Hkv = 64, 1
+    mem = Paged([100, 100], Hkv, d, seed=52)
+    q = randn(10, 2, d, seed=53)
+    for cu in ([0, 6, 4], [0, 4, 11], [1, 4, 10], [0, -1, 10]):
+        tok = bsa.Tokens(N=10, B=2, Hq=2, Hkv=Hkv, d=d, T=mem.T, cu_seqlens=ints(cu),
+                         seq_lens=ints([100, 100]))
+        step = bsa.PackedAttention(tok)
+        step.o.fill_(77.0)
+        step.lse.fill_(77.0)
+        step.run(q, *mem.caches())
+        assert int(step.status.item()) == bsa.BSA_DEV_BAD_LENGTH
+        assert (step.o == 77.0).all() and (step.lse == 77.0).all()
+    # a sequence shorter than its rows: the first ones see nothing
+    step = run_attend(q, mem, [0, 5, 10], [3, 100], Hkv, status=bsa.BSA_DEV_BAD_LENGTH)
+    assert (step.lse[:2] == -math.inf).all() and not step.o[:2].any()
+    want = exact(q, mem, [0, 5, 10], [3, 100], True, 2)
+    check(step, want, 100, d)
+
+
+def test_many_short_sequences():
+    d, G, Hkv, B = 64, 2, 1, 1500
+    new = [1 + b % 3 for b in range(B)]
+    cu = sums(new)
+    K, V = randn(B, Hkv, 64, d, seed=54), randn(B, Hkv, 64, d, seed=55)
+    q = randn(cu[-1], G, d, seed=56)
+    tok = bsa.Tokens(N=cu[-1], B=B, Hq=G, Hkv=Hkv, d=d, T=64, cu_seqlens=ints(cu),
+                     seq_lens=ints([n + b % 50 for b, n in enumerate(new)]))
+    step = bsa.PackedAttention(tok)
+    step.run(q, bsa.contiguous_cache(K), bsa.contiguous_cache(V))
+    lens = [n + b % 50 for b, n in enumerate(new)]
+
+    class Flat:
+        pass
+    mem = Flat()
+    mem.K, mem.V = K, V
+    kk, vv = f64(K), f64(V)
+    mem.keys = lambda X, b, n: (kk if X is K else vv)[b, :, :n]
+    check(step, exact(q, mem, cu, lens, True, G), 64, d)
+
+
+def test_graph_replay_with_new_lengths_and_a_second_stream():
+    d, G, Hkv = 128, 4, 2
+    mem = Paged([700, 700, 700], Hkv, d, seed=60)
+    N = 300
+    q = randn(N, Hkv * G, d, seed=61)
+    cu, lens = ints([0, 100, 200, 300]), ints([700, 700, 700])
+    tok = bsa.Tokens(N=N, B=3, Hq=Hkv * G, Hkv=Hkv, d=d, T=mem.T, cu_seqlens=cu, seq_lens=lens)
+    step = bsa.PackedAttention(tok)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step.run(q, *mem.caches())
+    side.synchronize()
+    first = step.o.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, capture_error_mode="relaxed"):
+        step.run(q, *mem.caches())
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(step.o, first)
+    for cu1, len1 in (([0, 1, 2, 3], [700, 1, 350]), ([0, 0, 299, 299], [9, 640, 0])):
+        cu.copy_(ints(cu1))
+        lens.copy_(ints(len1))
+        for _ in range(2):
+            g.replay()
+        torch.cuda.synchronize()
+        assert int(step.status.item()) == 0
+        part = Paged.__new__(Paged)
+        part.__dict__.update(mem.__dict__)
+        want = exact(q, part, cu1, len1, True, G)
+        # the pools hold garbage only behind 700, so shorter lengths read real keys
+        check(step, want, 700, d)
+
+
+# ------------------------------------------------------------------ shared prefixes
+def run_shared(q, mem, cu, lens, Hkv, own, **kw):
+    N, Hq, d = q.shape
+    tok = bsa.Tokens(N=N, B=len(lens), Hq=Hq, Hkv=Hkv, d=d, T=mem.T, cu_seqlens=ints(cu),
+                     seq_lens=ints(lens))
+    step = bsa.SharedPrefixDecode(tok)
+    for x in (step.o, step.lse, step.o_f32):
+        x.fill_(77.0)
+    step.run(q, *mem.caches(), *own)
+    assert int(step.status.item()) == 0
+    for x in (step.o, step.lse, step.o_f32):
+        assert (x[cu[-1]:] == 77.0).all()
+    return step
+
+
+def exact_shared(q, mem, cu, lens, G, own):
+    o, lse, spread, size = exact(q, mem, cu, lens, False, G)
+    if own[0] is None:
+        return o, lse, spread, size
+    oo, ll = f64(own[0]), f64(own[1])
+    live = ~np.isnan(lse)
+    om, lm, wa, wb = TO.merge(o, np.where(live, lse, 0.0), oo, ll)
+    spread = wa[..., None] * spread + np.where(wb[..., None] > 0, np.abs(oo), 0.0) * wb[..., None]
+    return om, np.where(live, lm, np.nan), spread, size
+
+
+@pytest.mark.parametrize("d,G", [(64, 1), (128, 4), (128, 16)])
+@pytest.mark.parametrize("rows,lens", [([1], [1]), ([40], [777]), ([3, 0, 65, 2], [600, 64, 1, 0])])
+@pytest.mark.parametrize("with_own", [True, False])
+def test_shared_prefix(d, G, rows, lens, with_own):
+    Hkv = 2
+    cu = sums(rows)
+    N = cu[-1] + 2
+    mem = Paged(lens, Hkv, d, seed=70)
+    q = randn(N, Hkv * G, d, seed=71, scale=1.5)
+    own = (None, None)
+    if with_own:
+        o_own = torch.randn(N, Hkv * G, d, generator=gen(72), device="cuda")
+        lse_own = 5.0 + 3.0 * torch.randn(N, Hkv * G, generator=gen(73), device="cuda")
+        lse_own[0, 0] = -math.inf           # a sequence with no tokens of its own yet
+        o_own[0, 0] = float("nan")
+        own = (o_own, lse_own)
+    step = run_shared(q, mem, cu, lens, Hkv, own)
+    check(step, exact_shared(q, mem, cu, lens, G, own), max(lens), d)
+
+
+def test_shared_prefix_outputs_may_be_the_own_part():
+    d, G, Hkv = 128, 4, 2
+    mem = Paged([300], Hkv, d, seed=74)
+    q = randn(9, Hkv * G, d, seed=75)
+    o_own = torch.randn(9, Hkv * G, d, generator=gen(76), device="cuda")
+    lse_own = torch.randn(9, Hkv * G, generator=gen(77), device="cuda") + 5
+    step = run_shared(q, mem, [0, 9], [300], Hkv, (o_own, lse_own))
+    bsa.bsa_decode_shared(step.tok, q, *mem.caches(), o_own, lse_own, step.o, lse_own, o_own,
+                          step.workspace, step.status)
+    assert torch.equal(o_own, step.o_f32) and torch.equal(lse_own, step.lse)
+
+
+# ------------------------------------------------------------------ together
+def test_prompt_append_attend_then_shared_decode():
+    """As a server runs them: a shared document and the sequences' own prompts are appended
+    (normed and rotated) and attended; then a decode step appends a token to every sequence,
+    block-sparse decode covers its own tokens and the document is joined to it."""
+    d, Hq, Hkv, G, B, doc = 128, 8, 2, 4, 3, 333
+    own_lens = [70, 1, 200]
+    g = gen(80)
+    T = 320
+    nb = T // 64
+    pages = 6 + B * nb
+    K, V, I = (torch.full((pages, Hkv, 64, w), float("nan"), dtype=torch.bfloat16, device="cuda")
+               for w in (d, d, 16))
+    pt = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)
+    doc_pt, own_pt = pt[:6].reshape(1, 6).contiguous(), pt[6:].reshape(B, nb).contiguous()
+    rope = bsa.Rope.make(d, theta=500000.0)
+    w = (1.0 + 0.1 * torch.randn(d, generator=g, device="cuda")).float()
+    common = dict(Hq=Hq, Hkv=Hkv, d=d, rope=rope, norm=True, q_weight=w, k_weight=w)
+    f, _ = bsa.rope_frequencies(d, 500000.0)
+    new = lambda n: [torch.randn(n, h, x, generator=g, device="cuda").to(torch.bfloat16)
+                     for h, x in ((Hq, d), (Hkv, d), (Hkv, d), (Hkv, 16))]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def append(tok, x, table):
+        q, k, v, idx = x
+        q_out = torch.empty_like(q)
+        bsa.bsa_append_kv(tok, k, v, bsa.paged_cache(K, table), bsa.paged_cache(V, table), idx,
+                          bsa.paged_cache(I, table), q, q_out, status)
+        return q_out
+
+    # the document
+    x_doc = new(doc)
+    tok = bsa.Tokens(N=doc, B=1, T=6 * 64, seq_lens=ints([doc]), **common)
+    q_doc = append(tok, x_doc, doc_pt)
+    att = bsa.PackedAttention(tok)
+    att.run(q_doc, bsa.paged_cache(K, doc_pt), bsa.paged_cache(V, doc_pt))
+    mem = Paged.__new__(Paged)
+    mem.K, mem.V, mem.pt, mem.T = K, V, doc_pt, 6 * 64
+    check(att, exact(q_doc, mem, [0, doc], [doc], True, G), doc, d)
+
+    # a decode step: the sequences' tokens so far, then one more each
+    for lens, rows in ((own_lens, own_lens), ([n + 1 for n in own_lens], [1] * B)):
+        cu = sums(rows)
+        x = new(cu[-1])
+        pos = np.concatenate([doc + n - c + np.arange(c) for n, c in zip(lens, rows)])
+        tok = bsa.Tokens(N=cu[-1], B=B, T=T, cu_seqlens=ints(cu), seq_lens=ints(lens),
+                         positions=ints(pos.tolist()), **common)
+        q = append(tok, x, own_pt)
+        want_q = TO.norm_rope(f64(x[0]), pos, f, weight=f64(w), eps=1e-6, norm=True)
+        assert (np.abs(f64(q) - want_q[0]) <= 2.0 ** -8 * np.abs(want_q[0]) + 2.0 ** -19 * want_q[1]).all()
+    prob = bsa.Problem(phase=bsa.PHASE_DECODE, B=B, Hq=Hq, Hkv=Hkv, d=d, T=T, n_sink=1, n_local=2,
+                       k_max=8, p=1.0, seq_lens=ints(lens))
+    sparse = bsa.DecodeStep(prob)
+    q_idx = torch.randn(B, Hq, 16, generator=g, device="cuda").to(torch.bfloat16)
+    for page in own_pt.flatten().tolist():       # block-sparse decode wants finite rows
+        K[page], V[page], I[page] = K[page].nan_to_num(), V[page].nan_to_num(), I[page].nan_to_num()
+    sparse.run(q, q_idx, bsa.paged_cache(I, own_pt), bsa.paged_cache(K, own_pt),
+               bsa.paged_cache(V, own_pt))
+    assert int(sparse.status.item()) == 0 and int(status.item()) == 0
+    tok = bsa.Tokens(N=B, B=1, Hq=Hq, Hkv=Hkv, d=d, T=6 * 64, seq_lens=ints([doc]))
+    shared = bsa.SharedPrefixDecode(tok)
+    shared.run(q, bsa.paged_cache(K, doc_pt), bsa.paged_cache(V, doc_pt), sparse.o_f32, sparse.lse)
+    # every block was kept: the sum is dense attention over the document and all own tokens
+    kd, vd = mem.keys(K, 0, doc), mem.keys(V, 0, doc)
+    want = [np.zeros((B, Hq, d)), np.zeros((B, Hq)), np.zeros((B, Hq, d)), np.zeros((B, Hq))]
+    mem.pt = own_pt
+    for b, n in enumerate(lens):
+        ko, vo = mem.keys(K, b, n), mem.keys(V, b, n)
+        for h in range(Hq):
+            kk, vv = np.concatenate([kd[h // G], ko[h // G]]), np.concatenate([vd[h // G], vo[h // G]])
+            r = TO.attend_rows(f64(q)[b:b + 1, h], kk, vv, 1 / math.sqrt(d), np.ones((1, len(kk)), bool))
+            for a, y in zip(want, r):
+                a[b, h] = y[0]
+    check(shared, want, doc + max(lens), d)
