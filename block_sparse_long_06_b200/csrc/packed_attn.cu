@@ -12,16 +12,16 @@
 //    in shared memory. A unit is two such tiles (256/G tokens) of one kv head, so a key tile
 //    is read once for 256 rows, and a single token still fills G rows.
 //  * A step is 128 keys (two blocks of the cache). The loader warp copies K and V of a step
-//    into a ring of 32 KB stages; one issuing thread per tile runs S = Q K^T into the tile's
-//    128 columns of tensor memory and O += P V from it; 4 softmax warps per tile (one row a
-//    thread, so row maxima and sums need no shuffles) turn S into P, written as bf16 over S.
-//    The two tiles take turns: while one is in its softmax, the other has the tensor cores.
-//    P V (j) and S (j + 1) of a tile are issued by the same thread, in order, so S needs no
-//    second buffer and the arrival of S (j + 1) says that P V (j) is done.
+//    into a ring of 32 KB stages; one issuing thread runs S = Q K^T into the tile's 128
+//    columns of tensor memory and O += P V from it; 8 softmax warps per tile (two threads a
+//    row, 64 keys each) turn S into P, written as bf16 over S. The two tiles take turns:
+//    while one is in its softmax, the other has the tensor cores. P V (j) and S (j + 1) of a
+//    tile are issued by the same thread, in order, so S needs no second buffer and the
+//    arrival of S (j + 1) says that P V (j) is done.
 //  * The running maximum only moves when it grows by more than 8 (log2): O is then rescaled
-//    in tensor memory. P <= 2^8 is rounded to bf16 (half a step is 2^-9 of each term, below
-//    the 2^-9 rounding of the bf16 output once the terms' errors average); l sums the fp32
-//    values. V stays bf16, so no value range is lost.
+//    in tensor memory. P <= 2^8 is rounded to bf16 (at most 2^-8 of each term, as much as the
+//    output's own rounding, and averaged over a row's terms); l sums the fp32 values. V stays
+//    bf16, so no value range is lost.
 //  * Few rows over many keys: the plan kernel (one block) cuts units into splits of the key
 //    axis, until the SMs are filled; each writes its O, m and l in fp32 and the merge kernel
 //    joins them. Units are handed out longest first, one kv head after the other, so the
@@ -38,8 +38,8 @@
 namespace bsa {
 namespace {
 
-constexpr int kThreads = 384;          // warp 0 loads, 1-2 issue, 3 patches, 4-7 / 8-11 softmax
-constexpr int kWarpLoad = 0, kWarpMma = 1, kWarpPatch = 3, kWarpSm = 4;
+constexpr int kThreads = 640;          // warps 0-7 / 8-15: softmax of tile 0 / 1; the last four:
+constexpr int kSoftmaxWarps = 16, kWarpLoad = 16, kWarpMma = 17, kWarpPatch = 18;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kStep = 128;             // keys a step
 constexpr int kMaxStages = 10;
@@ -66,8 +66,11 @@ struct Bars {
   uint64_t info_full[2], info_empty[2];
   uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], kv_raw[kMaxStages];
-  uint64_t s_full[2], p_ready[2], o_full[2];
-  uint64_t mma_done[2];
+  uint64_t s_full[2], o_full[2];
+  uint64_t p_ready[2][2];              // [tile][first or second 32 keys of each 64]
+  uint64_t pair[2][4];                 // [tile][quarter of its rows]: the two warps of the rows
+  uint64_t mma_done;
+  float swap[2][2][128];               // [tile][half of the keys][row]: maxima, sums
   Unit info[2];
   uint32_t tmem_base;
   int abort_flag;
@@ -75,7 +78,7 @@ struct Bars {
 
 template <int D>
 constexpr int smem_bytes() {
-  return Cfg<D>::kOffBar + static_cast<int>(sizeof(Bars)) + 1024;
+  return Cfg<D>::kOffBar + static_cast<int>(sizeof(Bars));
 }
 static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory");
 
@@ -95,6 +98,16 @@ BSA_DEVFN bool warp_wait_sleep(uint64_t* bar, uint32_t parity) {
   bool ok = true;
   if ((threadIdx.x & 31) == 0) ok = mbar_wait_sleep(bar, parity);
   return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+
+// Every lane polls (one broadcast read a try): no shuffle behind the wait. Warp-uniform.
+BSA_DEVFN bool warp_wait_all(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
+}
+
+// The same for waits that are long: the warp sleeps instead of polling.
+BSA_DEVFN bool warp_sleep_all(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait_sleep(bar, parity)) != 0;
 }
 
 BSA_DEVFN float max3(float x, float y, float z) {
@@ -284,27 +297,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap tmv) {
   using C = Cfg<D>;
   constexpr int NS = C::kStages;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) unsigned char smem[];   // the swizzle needs 1024-byte tiles
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kOffBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int half_tok = 128 / a.G;      // tokens of one tile
+  if ((smem_u32(smem) & 1023u) != 0) {   // dynamic shared memory starts on a 1 KB boundary
+    if (threadIdx.x == 0) report(a.status, BSA_DEV_TIMEOUT);
+    return;
+  }
 
   if (threadIdx.x == 0) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars->info_full[x], 1);
-      mbar_init(&bars->info_empty[x], 11);   // 2 issuers, the patch warp, 8 softmax warps
+      mbar_init(&bars->info_empty[x], 2 + kSoftmaxWarps);   // with the issuer and the patch warp
       mbar_init(&bars->q_full[x], 1);
       mbar_init(&bars->q_empty[x], 1);
       mbar_init(&bars->s_full[x], 1);
-      mbar_init(&bars->p_ready[x], 4);
+      mbar_init(&bars->p_ready[x][0], 8);    // the tile's softmax warps
+      mbar_init(&bars->p_ready[x][1], 8);
+      for (int y = 0; y < 4; ++y) mbar_init(&bars->pair[x][y], 2);
       mbar_init(&bars->o_full[x], 1);
-      mbar_init(&bars->mma_done[x], 1);
     }
+    mbar_init(&bars->mma_done, 1);
     for (int s = 0; s < NS; ++s) {
       mbar_init(&bars->kv_full[s], 1);
-      mbar_init(&bars->kv_empty[s], 2);      // both issuers
+      mbar_init(&bars->kv_empty[s], 1);
       mbar_init(&bars->kv_raw[s], 1);
     }
     bars->abort_flag = 0;
@@ -320,8 +337,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = bars->tmem_base;
   grid_dependency_wait();
 
-  if (warp < kWarpSm) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (warp >= kSoftmaxWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == kWarpLoad) {
       // ---------------------------------------------------------------- Q / K / V
       const int entries = a.head[0];
@@ -465,92 +482,139 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         kc += 2 * max(0, n);
       }
-    } else if (lane == 0) {
-      // ------------------------------------------------------ MMA issuer of tile t
-      const int t = warp - kWarpMma;
+    } else if (warp == kWarpMma && tc::elect()) {
+      // ------------------------------------------------- MMA issuer of both tiles
+      // One thread, the tiles in turn: P V (j) and S (j + 1) of tile 0, then of tile 1. The
+      // tensor cores work in that order, so the tiles' softmax phases are half a period
+      // apart (with an issuer for each tile both were in their softmax, then both on the
+      // tensor cores: 5900 cycles a step at d = 128).
       const uint32_t idS = tc::idesc_f16(128, kStep, 1, false);
       const uint32_t idPV = tc::idesc_f16(128, D, 1, true);
       const uint32_t sbase = smem_u32(smem);
-      const uint64_t dq = tc::smem_desc_sw128(sbase + t * C::kTile, 16, 1024);
-      const uint32_t s_tm = tmem + 256 + 128 * t, o_tm = tmem + 128 * t;
-      uint32_t un = 0, kc = 0, qc = 0, pc = 0;
-      bool ok = true;
-      auto full = [&](uint32_t k) { return mbar_wait_sleep(&bars->kv_full[k % NS], (k / NS) & 1); };
-      auto scores = [&](uint32_t k) {
-        const uint64_t dk = tc::smem_desc_sw128(sbase + C::kOffKV + (k % NS) * C::kTile, 16, 1024);
+      const uint64_t dq0 = tc::smem_desc_sw128(sbase, 16, 1024);
+      const uint64_t dk0 = tc::smem_desc_sw128(sbase + C::kOffKV, 16, 1024);
+      const uint64_t dv0 = tc::smem_desc_sw128(sbase + C::kOffKV, C::kSlab, 1024);
+      uint32_t un = 0, q_phase = 0, p_phase = 0;   // a bit for each tile
+      int st = 0;                                  // the ring's stage and its phase
+      uint32_t kv_phase = 0;
+      int n = 0, nt = 0;
+      // the next unit that has keys; n = 0 at the end. False: a wait gave up.
+      auto fetch = [&]() {
+        while (true) {
+          const int slot = un & 1;
+          if (!mbar_wait_sleep(&bars->info_full[slot], (un >> 1) & 1)) return false;
+          const Unit U = bars->info[slot];
+          mbar_arrive(&bars->info_empty[slot]);
+          ++un;
+          const bool stop = U.u < 0 || aborted(bars);
+          n = stop ? 0 : U.step1 - U.step0;
+          nt = U.ntok > half_tok ? 2 : 1;
+          if (stop || n > 0) return true;
+        }
+      };
+      auto full = [&]() { return mbar_wait(&bars->kv_full[st], kv_phase); };
+      auto next_stage = [&]() {
+        if (++st == NS) {
+          st = 0;
+          kv_phase ^= 1;
+        }
+      };
+      auto scores = [&](int t, int stage, bool last) {
+        const uint64_t dq = dq0 + ((t * C::kTile) >> 4), dk = dk0 + ((stage * C::kTile) >> 4);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint64_t off = ((ks >> 2) * C::kSlab + (ks & 3) * 32) >> 4;
-          tc::mma_ss(s_tm, dq + off, dk + off, idS, ks > 0);
+          tc::mma_ss(tmem + 256 + 128 * t, dq + off, dk + off, idS, ks > 0);
         }
         tc::commit(&bars->s_full[t]);
-        tc::commit(&bars->kv_empty[k % NS]);
+        if (last) tc::commit(&bars->q_empty[t]);   // Q is free after the unit's last scores
       };
-      while (ok) {
-        const int slot = un & 1;
-        if (!mbar_wait_sleep(&bars->info_full[slot], (un >> 1) & 1)) { ok = false; break; }
-        const Unit U = bars->info[slot];
-        mbar_arrive(&bars->info_empty[slot]);
-        ++un;
-        if (U.u < 0 || aborted(bars)) break;
-        const int n = U.step1 - U.step0;
-        if (n <= 0) continue;
-        if (t == 1 && U.ntok <= half_tok) {
-          // no rows: the stages are free as far as this tile goes
-          for (int j = 0; j < 2 * n && ok; ++j, ++kc) {
-            ok = full(kc);
-            if (ok) mbar_arrive(&bars->kv_empty[kc % NS]);
-          }
-          continue;
-        }
-        if (!mbar_wait_sleep(&bars->q_full[t], qc & 1)) { ok = false; break; }
-        ++qc;
-        if (!full(kc)) { ok = false; break; }
-        tc::fence_after_sync();
-        scores(kc);
-        if (n == 1) tc::commit(&bars->q_empty[t]);
-        for (int j = 0; j < n; ++j) {
-          const uint32_t kv = kc + 2 * j + 1;   // the stage of V (j); K (j + 1) is the next one
-          if (!mbar_wait_sleep(&bars->p_ready[t], pc & 1)) { ok = false; break; }
-          ++pc;
-          if (!full(kv)) { ok = false; break; }
+      bool ok = fetch();
+      while (ok && n > 0) {
+        if (!full()) { ok = false; break; }
+        for (int t = 0; t < nt && ok; ++t) {
+          ok = mbar_wait(&bars->q_full[t], (q_phase >> t) & 1);
+          if (!ok) break;
+          q_phase ^= 1u << t;
           tc::fence_after_sync();
-          const uint64_t dv =
-              tc::smem_desc_sw128(sbase + C::kOffKV + (kv % NS) * C::kTile, C::kSlab, 1024);
-#pragma unroll
-          for (int kk = 0; kk < kStep / 16; ++kk)
-            tc::mma_ts(o_tm, s_tm + kk * 8, dv + ((kk * 2048) >> 4), idPV, j > 0 || kk > 0);
-          tc::commit(&bars->kv_empty[kv % NS]);
-          if (j + 1 < n) {
-            if (!full(kv + 1)) { ok = false; break; }
+          scores(t, st, n == 1);
+        }
+        if (!ok) break;
+        tc::commit(&bars->kv_empty[st]);
+        next_stage();
+        for (int j = 0; j < n && ok; ++j) {
+          const int sv = st;             // the stage of V (j); K (j + 1) is the next one
+          for (int t = 0; t < nt; ++t) {
+            const uint32_t s_tm = tmem + 256 + 128 * t, o_tm = tmem + 128 * t;
+            const uint32_t phase = (p_phase >> t) & 1;
+            p_phase ^= 1u << t;
+            if (!mbar_wait(&bars->p_ready[t][0], phase)) { ok = false; break; }
+            if (t == 0) {
+              ok = full();
+              next_stage();
+              if (!ok) break;
+            }
             tc::fence_after_sync();
-            scores(kv + 1);
-            if (j + 2 == n) tc::commit(&bars->q_empty[t]);   // Q is free after the last scores
-          } else {
-            tc::commit(&bars->o_full[t]);
+            const uint64_t dv = dv0 + ((sv * C::kTile) >> 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {   // keys 0-31 and 64-95
+              const int kk = i < 2 ? i : i + 2;
+              tc::mma_ts(o_tm, s_tm + kk * 8, dv + ((kk * 2048) >> 4), idPV, j > 0 || i > 0);
+            }
+            if (!mbar_wait(&bars->p_ready[t][1], phase)) { ok = false; break; }
+            tc::fence_after_sync();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int kk = i < 2 ? i + 2 : i + 4;
+              tc::mma_ts(o_tm, s_tm + kk * 8, dv + ((kk * 2048) >> 4), idPV, true);
+            }
+            const bool more = j + 1 < n;
+            if (more) {
+              if (t == 0 && !full()) { ok = false; break; }
+              tc::fence_after_sync();
+              scores(t, st, j + 2 == n);
+            } else {
+              tc::commit(&bars->o_full[t]);
+            }
+          }
+          if (!ok) break;
+          tc::commit(&bars->kv_empty[sv]);
+          if (j + 1 < n) {
+            tc::commit(&bars->kv_empty[st]);
+            next_stage();
           }
         }
-        kc += 2 * n;
+        if (ok) ok = fetch();
       }
       if (!ok) set_abort(bars, a.status);
       // every MMA this thread issued must finish before tensor memory is freed (bounded)
-      tc::commit(&bars->mma_done[t]);
-      mbar_wait_sleep(&bars->mma_done[t], 0, 200000000ull);
+      tc::commit(&bars->mma_done);
+      mbar_wait_sleep(&bars->mma_done, 0, 200000000ull);
     }
   } else {
     // ------------------------------------------------------------------ softmax of tile t
-    // Warp w has the tile's rows 32 (w % 4) .. + 31 (its quarter of tensor memory), one a
-    // thread.
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int t = (warp - kWarpSm) >> 2;
-    const int row = (warp & 3) * 32 + lane;
-    const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    // Two threads a row, in warps w and w + 4 (a warp reaches the quarter w % 4 of tensor
+    // memory's rows): each has 64 of a step's 128 keys, and half of O's columns when it is
+    // rescaled or written. They swap row maxima (and, at the end, sums) through shared memory.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    const int t = warp >> 3, hf = (warp >> 2) & 1, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_col = tmem + lane_addr + 256 + 128 * t;
-    const uint32_t o_col = tmem + lane_addr + 128 * t;
+    const uint32_t o_col = tmem + lane_addr + 128 * t + hf * (D / 2);
     const int tok = t * half_tok + row / a.G, hh = row % a.G;
-    const int warp_tok = t * half_tok + ((warp & 3) * 32) / a.G;   // of the warp's first row
+    const int warp_tok = t * half_tok + (quarter * 32) / a.G;   // of the warp's first row
     const float sc = a.scale_log2;
-    uint32_t un = 0, stepc = 0, oc = 0;
+    float* mine = &bars->swap[t][hf][row];
+    const float* theirs = &bars->swap[t][hf ^ 1][row];
+    uint64_t* pair = &bars->pair[t][quarter];
+    uint32_t un = 0, stepc = 0, oc = 0, swaps = 0;
+    // both threads of each row have written `mine`; theirs can be read
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair);
+      return warp_wait_all(pair, swaps++ & 1);
+    };
     while (true) {
       const int slot = un & 1;
       if (!warp_wait(&bars->info_full[slot], (un >> 1) & 1)) {
@@ -569,49 +633,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY;
       float2 l = make_float2(0.f, 0.f);
       bool ok = true;
-      const bool idle = warp_tok >= U.ntok;   // no row of this warp exists
+      const bool idle = warp_tok >= U.ntok;   // no row of this warp (and the other) exists
       for (int step = U.step0; step < U.step1; ++step, ++stepc) {
-        if (!warp_wait(&bars->s_full[t], stepc & 1)) { ok = false; break; }
+        if (!warp_sleep_all(&bars->s_full[t], stepc & 1)) { ok = false; break; }
         if (idle) {   // rows of P that nobody reads
-          if (lane == 0) mbar_arrive(&bars->p_ready[t]);
+          if (lane == 0) {
+            mbar_arrive(&bars->p_ready[t][0]);
+            mbar_arrive(&bars->p_ready[t][1]);
+          }
           continue;
         }
         tc::fence_after_sync();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tc::ld32(s_col + 32 * i, s[i]);
+        uint32_t s[2][32];
+        tc::ld32(s_col + 64 * hf, s[0]);
+        tc::ld32(s_col + 64 * hf + 32, s[1]);
         tc::wait_ld();
-        const int lim = last - step * kStep;   // columns 0 .. lim are visible
-        if (lim < kStep - 1) {
+        const int lim = last - step * kStep - 64 * hf;   // columns 0 .. lim are visible
+        if (lim < 63) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int c = 0; c < 32; ++c)
               if (32 * i + c > lim) s[i][c] = 0xff800000u;
         }
         if (U.bad) {
-          for (int x = 0; x < 2; ++x) {
-            const int blk = 2 * step + x;
-            if (blk * kBlock < U.len && (block_row(a.k, U.b, U.g, blk, U.len, D) < 0 ||
-                                         block_row(a.v, U.b, U.g, blk, U.len, D) < 0)) {
+          const int blk = 2 * step + hf;
+          if (blk * kBlock < U.len && (block_row(a.k, U.b, U.g, blk, U.len, D) < 0 ||
+                                       block_row(a.v, U.b, U.g, blk, U.len, D) < 0)) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int c = 0; c < 32; ++c)
-                  if ((i >> 1) == x) s[i][c] = 0xff800000u;
-            }
+              for (int c = 0; c < 32; ++c) s[i][c] = 0xff800000u;
           }
         }
         float mx[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          mx[i] = max3(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]), __uint_as_float(s[i][2]));
+          const uint32_t* v = &s[i >> 1][(i & 1) * 16];
+          mx[i] = max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
 #pragma unroll
-          for (int c = 3; c < 31; c += 2)
-            mx[i] = max3(mx[i], __uint_as_float(s[i][c]), __uint_as_float(s[i][c + 1]));
-          mx[i] = fmaxf(mx[i], __uint_as_float(s[i][31]));
+          for (int c = 3; c < 15; c += 2)
+            mx[i] = max3(mx[i], __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+          mx[i] = fmaxf(mx[i], __uint_as_float(v[15]));
         }
-        const float x = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+        const float part = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        *mine = part;
+        tc::fence_before_sync();   // S is in registers: the other thread may write P over it
+        if (!meet()) { ok = false; break; }
+        tc::fence_after_sync();
+        const float x = fmaxf(part, *theirs) * sc;
         const bool up = x > m + 8.0f;
         const float f = up ? ex2(m - x) : 1.0f;
         if (__any_sync(0xffffffffu, up)) {
@@ -623,35 +693,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (step > U.step0) {
             // the tile's P V of the last step is done (its S was issued behind it)
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t ov[32];
-              tc::ld32(o_col + c, ov);
+            for (int c = 0; c < D / 2; c += 16) {
+              uint32_t ov[16];
+              tc::ld16(o_col + c, ov);
               tc::wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f);
-              tc::st32(o_col + c, ov);
+              for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f);
+              tc::st16(o_col + c, ov);
             }
           }
         }
         const float neg = m == -INFINITY ? 0.f : -m;
         const float2 neg2 = make_float2(neg, neg), sc2 = make_float2(sc, sc);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int h = 0; h < 2; ++h) {   // the P V of the first 32 keys of each 64 starts early
+          uint32_t p[16];
 #pragma unroll
           for (int c = 0; c < 32; c += 2) {
             const float2 v = __ffma2_rn(
-                make_float2(__uint_as_float(s[i][c]), __uint_as_float(s[i][c + 1])), sc2, neg2);
-            const float2 p = make_float2(ex2(v.x), ex2(v.y));
-            l = __fadd2_rn(l, p);
-            s[i >> 1][(i & 1) * 16 + c / 2] = pack_bf16(p.x, p.y);
+                make_float2(__uint_as_float(s[h][c]), __uint_as_float(s[h][c + 1])), sc2, neg2);
+            const float2 e = make_float2(ex2(v.x), ex2(v.y));
+            l = __fadd2_rn(l, e);
+            p[c / 2] = pack_bf16(e.x, e.y);
           }
+          tc::st16(s_col + 32 * hf + 16 * h, p);
+          tc::wait_st();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->p_ready[t][h]);
         }
-        tc::st32(s_col, s[0]);
-        tc::st32(s_col + 32, s[1]);
-        tc::wait_st();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_ready[t]);
       }
       if (!ok || aborted(bars)) {
         if (lane == 0) set_abort(bars, a.status);
@@ -659,57 +729,64 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ---- epilogue
       const bool empty = U.step1 <= U.step0;
-      if (!empty) {
-        if (!warp_wait(&bars->o_full[t], oc & 1)) {
-          if (lane == 0) set_abort(bars, a.status);
-          break;
-        }
-        ++oc;
-        tc::fence_after_sync();
+      if (idle) {
+        if (!empty) ++oc;
+        continue;
       }
-      const float L = l.x + l.y;
+      *mine = l.x + l.y;
+      if (!meet() || (!empty && !warp_sleep_all(&bars->o_full[t], oc++ & 1))) {
+        if (lane == 0) set_abort(bars, a.status);
+        break;
+      }
+      tc::fence_after_sync();
+      // the same order in both threads
+      const float L = hf ? *theirs + (l.x + l.y) : (l.x + l.y) + *theirs;
       const bool part = U.nsplit > 1 || a.partial;
       const float inv = part ? 1.0f : L == 0.f ? 0.f : 1.0f / L;
       const int64_t at = (static_cast<int64_t>(U.row0) + tok) * a.Hq + U.g * a.G + hh;
       const int64_t pat = static_cast<int64_t>(U.split) * a.N * a.Hq + at;
-      if (!idle) {
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t ov[32];
-          if (empty) {
+      for (int c = 0; c < D / 2; c += 32) {
+        uint32_t ov[32];
+        if (empty) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) ov[i] = 0u;
-          } else {
-            tc::ld32(o_col + c, ov);
-            tc::wait_ld();
-          }
-          if (live) {
-            float v[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(ov[i]) * inv;
-            if (!part) {
-              uint4* ob = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + at * D + c);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                ob[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                                   pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
-            }
-            float* of = part ? a.part_o + pat * D + c : a.o_f32 != nullptr ? a.o_f32 + at * D + c : nullptr;
-            if (of != nullptr) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                reinterpret_cast<float4*>(of)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-            }
-          }
+          for (int i = 0; i < 32; ++i) ov[i] = 0u;
+        } else {
+          tc::ld32(o_col + c, ov);
+          tc::wait_ld();
         }
         if (live) {
-          if (part)
-            *reinterpret_cast<float2*>(a.part_ml + 2 * pat) = make_float2(m, L);
-          else
-            a.lse[at] = L == 0.f ? -INFINITY : (m + log2f(L)) * kLn2;
+          const int cc = hf * (D / 2) + c;
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(ov[i]) * inv;
+          if (!part) {
+            uint4* ob = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + at * D + cc);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              ob[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                                 pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+          }
+          float* of = part ? a.part_o + pat * D + cc : a.o_f32 != nullptr ? a.o_f32 + at * D + cc : nullptr;
+          if (of != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              reinterpret_cast<float4*>(of)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
         }
       }
+      if (live && hf == 0) {
+        if (part)
+          *reinterpret_cast<float2*>(a.part_ml + 2 * pat) = make_float2(m, L);
+        else
+          a.lse[at] = L == 0.f ? -INFINITY : (m + log2f(L)) * kLn2;
+      }
       tc::fence_before_sync();
+      // the sums have been read before the next unit's first maxima are written
+      if (!meet()) {
+        if (lane == 0) set_abort(bars, a.status);
+        break;
+      }
     }
   }
 
