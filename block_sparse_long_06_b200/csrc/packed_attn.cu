@@ -10,7 +10,9 @@
 //  * The G query heads of a kv group are rows of the same tile: row r of a 128-row tile is
 //    token r / G, head r % G, which is how one TMA box {64, G, 128/G} of q [N, Hq, d] lands
 //    in shared memory. A unit is two such tiles (256/G tokens) of one kv head, so a key tile
-//    is read once for 256 rows, and a single token still fills G rows.
+//    is read once for 256 rows, and a single token still fills G rows. A unit of up to 128
+//    rows gives both tiles of tensor memory the same rows and its steps in turn; their
+//    results are joined when they are written.
 //  * A step is 128 keys (two blocks of the cache). The loader warp copies K and V of a step
 //    into a ring of 32 KB stages; one issuing thread runs S = Q K^T into the tile's 128
 //    columns of tensor memory and O += P V from it; 8 softmax warps per tile (two threads a
@@ -38,13 +40,16 @@
 namespace bsa {
 namespace {
 
-constexpr int kThreads = 640;          // warps 0-7 / 8-15: softmax of tile 0 / 1; the last four:
-constexpr int kSoftmaxWarps = 16, kWarpLoad = 16, kWarpMma = 17, kWarpPatch = 18;
+constexpr int kThreads = 384;          // warps 0-3 / 4-7: softmax of tile 0 / 1; then one each:
+constexpr int kSoftmaxWarps = 8, kWarpLoad = 8, kWarpMma = 9, kWarpPatch = 10;
+// of every kPolyOf pairs of a row's scores, kPoly take their exponentials by polynomial
+constexpr int kPolyOf = 8, kPoly = 1;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kStep = 128;             // keys a step
 constexpr int kMaxStages = 10;
 constexpr int kPlanThreads = 1024;
-constexpr int kBuckets = 512;
+constexpr int kBuckets = 512, kPlanTiles = 1024;
+constexpr float kUnitCost = 4.f;       // of a unit besides its steps, in steps of one tile
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -67,10 +72,10 @@ struct Bars {
   uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], kv_raw[kMaxStages];
   uint64_t s_full[2], o_full[2];
-  uint64_t p_ready[2][2];              // [tile][first or second 32 keys of each 64]
-  uint64_t pair[2][4];                 // [tile][quarter of its rows]: the two warps of the rows
+  uint64_t p_ready[2][2];              // [tile][half of the step's keys]
+  uint64_t pair[4];                    // [quarter of the rows]: its warps of both tiles
   uint64_t mma_done;
-  float swap[2][2][128];               // [tile][half of the keys][row]: maxima, sums
+  float2 swap[2][128];                 // [tile][row]: (m, l) of the tile
   Unit info[2];
   uint32_t tmem_base;
   int abort_flag;
@@ -114,6 +119,28 @@ BSA_DEVFN float max3(float x, float y, float z) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
   return r;
+}
+
+// 2^x on the FMA pipes, two lanes at once, for x <= 8: x = n + f with n the nearest integer
+// (adding 1.5 * 2^23 rounds it into the low mantissa bits), 2^f by a quartic of least relative
+// error on [-1/2, 1/2] among those that are exactly 1 at 0 (Remez exchange, exp2_poly_fit.py:
+// 3.6e-6, so the fp32 sum l keeps 18 bits; the bf16 P needs 9), n added to the exponent field.
+// x is clamped at -127, where that gives exactly 0: masked scores add nothing.
+BSA_DEVFN float2 exp2_poly(float2 x) {
+  constexpr float kC1 = 0.6931136250495911f, kC2 = 0.24020710587501526f;
+  constexpr float kC3 = 0.055976882576942444f, kC4 = 0.009782912209630013f;
+  constexpr float kShift = 12582912.0f;  // 1.5 * 2^23
+  x.x = fmaxf(x.x, -127.0f);
+  x.y = fmaxf(x.y, -127.0f);
+  const float2 r = __fadd2_rn(x, make_float2(kShift, kShift));
+  const float2 nn = __ffma2_rn(r, make_float2(-1.0f, -1.0f), make_float2(kShift, kShift));  // -n
+  const float2 f = __fadd2_rn(x, nn);
+  float2 p = __ffma2_rn(make_float2(kC4, kC4), f, make_float2(kC3, kC3));
+  p = __ffma2_rn(p, f, make_float2(kC2, kC2));
+  p = __ffma2_rn(p, f, make_float2(kC1, kC1));
+  p = __ffma2_rn(p, f, make_float2(1.0f, 1.0f));
+  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(r.x) << 23)),
+                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(r.y) << 23)));
 }
 
 // Row (of width d) of the first token of block blk of (b, g), or -1 where it is bad.
@@ -167,8 +194,8 @@ BSA_DEVFN Tile tile_of(const PackedArgs& a, int t) {
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) {
   __shared__ int warp_sum[32];
   __shared__ int carry, bad, longest;
-  __shared__ unsigned long long work;
-  __shared__ int bucket[kBuckets];
+  __shared__ unsigned long long work, best;   // best: (time, candidate)
+  __shared__ int bucket[kBuckets], costs[kPlanTiles];
   grid_dependency_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = packed_unit_tokens(a.G);
@@ -177,6 +204,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) 
     bad = 0;
     longest = 0;
     work = 0;
+    best = ~0ull;
   }
   for (int i = tid; i < kBuckets; i += kPlanThreads) bucket[i] = 0;
   __syncthreads();
@@ -213,11 +241,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) 
   const bool refuse = bad != 0;
   const int ntiles = refuse ? 0 : carry;
   if (refuse && tid == 0) report(a.status, BSA_DEV_BAD_LENGTH);
-  // steps of all tiles and of the longest
+  // cost of all tiles and of the costliest: a step of two 128-row tiles costs twice a step of one
+  const int half = per / 2;
+  auto cost_of = [&](const Tile& x) { return x.ntok > half ? 2 * x.steps : x.steps; };
   unsigned long long sum = 0;
   int top = 0;
   for (int t = tid; t < ntiles; t += kPlanThreads) {
-    const int c = tile_of(a, t).steps;
+    const int c = cost_of(tile_of(a, t));
+    if (t < kPlanTiles) costs[t] = c;
     sum += c;
     top = max(top, c);
   }
@@ -229,27 +260,44 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) 
     atomicMax(&longest, top);
   }
   __syncthreads();
-  // Steps a split may have. Without splits the SMs are evenly loaded where the longest unit
-  // is at most half of an SM's share, or where there are several units for each SM and the
-  // longest (started first) is no more than that share. Else about four splits for each SM,
-  // of at least 4 steps, so that the last ones to end are short.
-  const unsigned long long share = (work * a.Hkv + a.num_sms - 1) / a.num_sms;
-  int chunk = 1 << 30;
-  if (a.smax > 1 && !(2ull * longest <= share ||
-                      (static_cast<unsigned long long>(longest) <= share &&
-                       static_cast<long long>(ntiles) * a.Hkv >= 3ll * a.num_sms)))
-    chunk = max(4, static_cast<int>((share + 3) / 4));
+  // Without splits the SMs are evenly loaded where there are several units for each SM and the
+  // costliest (started first) is no more than an SM's share. Else the cost that a unit may have
+  // is searched, a warp for each candidate: the time is the costliest unit's where every unit
+  // has an SM of its own, and otherwise an SM's share of all costs and half of the costliest.
+  // A unit costs kUnitCost besides its steps (start, epilogue, its part of the merge).
+  const float share = static_cast<float>(work) * a.Hkv / a.num_sms;
+  int limit = 1 << 30;
+  if (a.smax > 1 && ntiles <= kPlanTiles &&
+      !(static_cast<float>(longest) <= share && static_cast<long long>(ntiles) * a.Hkv >= 3ll * a.num_sms)) {
+    const int cand = warp == 0 ? 1 << 30 : max(4, static_cast<int>(share * (0.1f + 0.06f * warp)) + 1);
+    int units = 0, piece = 0;
+    for (int t = lane; t < ntiles; t += 32) {
+      const int k = max(1, min(a.smax, (costs[t] + cand - 1) / cand));
+      units += k;
+      piece = max(piece, (costs[t] + k - 1) / k);
+    }
+    units = __reduce_add_sync(0xffffffffu, units) * a.Hkv;
+    piece = __reduce_max_sync(0xffffffffu, piece);
+    const float unit = piece + kUnitCost;
+    const float time = units <= a.num_sms ? unit : share + units * kUnitCost / a.num_sms + 0.5f * unit;
+    if (lane == 0) atomicMin(&best, (static_cast<unsigned long long>(__float_as_uint(time)) << 32) |
+                                        static_cast<unsigned>(cand));
+    __syncthreads();
+    limit = static_cast<int>(best & 0x7fffffffull);
+  }
   const int shift = max(0, 32 - __clz(longest) - 9);
-  auto splits_of = [&](int steps) { return max(1, min(a.smax, (steps + chunk - 1) / chunk)); };
-  auto bucket_of = [&](int steps, int n) {
-    return kBuckets - 1 - min(kBuckets - 1, ((steps + n - 1) / n) >> shift);
+  auto splits_of = [&](const Tile& x) {
+    return max(1, min(min(a.smax, x.steps), (cost_of(x) + limit - 1) / limit));
+  };
+  auto bucket_of = [&](const Tile& x, int n) {
+    return kBuckets - 1 - min(kBuckets - 1, ((cost_of(x) + n - 1) / n) >> shift);
   };
   bool any = false;
   for (int t = tid; t < ntiles; t += kPlanThreads) {
     const Tile x = tile_of(a, t);
-    const int n = splits_of(x.steps);
+    const int n = splits_of(x);
     any |= n > 1;
-    atomicAdd(&bucket[bucket_of(x.steps, n)], n);
+    atomicAdd(&bucket[bucket_of(x, n)], n);
   }
   any = __syncthreads_or(any) || a.partial;
   // exclusive sums of the buckets (kBuckets <= kPlanThreads)
@@ -272,8 +320,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) 
   __syncthreads();
   for (int t = tid; t < ntiles; t += kPlanThreads) {
     const Tile y = tile_of(a, t);
-    const int n = splits_of(y.steps);
-    const int at = atomicAdd(&bucket[bucket_of(y.steps, n)], n);
+    const int n = splits_of(y);
+    const int at = atomicAdd(&bucket[bucket_of(y, n)], n);
     for (int s = 0; s < n; ++s) {
       const int s0 = static_cast<int>(static_cast<int64_t>(y.steps) * s / n);
       const int s1 = static_cast<int>(static_cast<int64_t>(y.steps) * (s + 1) / n);
@@ -313,9 +361,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->q_full[x], 1);
       mbar_init(&bars->q_empty[x], 1);
       mbar_init(&bars->s_full[x], 1);
-      mbar_init(&bars->p_ready[x][0], 8);    // the tile's softmax warps
-      mbar_init(&bars->p_ready[x][1], 8);
-      for (int y = 0; y < 4; ++y) mbar_init(&bars->pair[x][y], 2);
+      mbar_init(&bars->p_ready[x][0], 4);    // the tile's softmax warps
+      mbar_init(&bars->p_ready[x][1], 4);
+      mbar_init(&bars->pair[2 * x], 2);
+      mbar_init(&bars->pair[2 * x + 1], 2);
       mbar_init(&bars->o_full[x], 1);
     }
     mbar_init(&bars->mma_done, 1);
@@ -338,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dependency_wait();
 
   if (warp >= kSoftmaxWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kWarpLoad) {
       // ---------------------------------------------------------------- Q / K / V
       const int entries = a.head[0];
@@ -495,10 +544,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dk0 = tc::smem_desc_sw128(sbase + C::kOffKV, 16, 1024);
       const uint64_t dv0 = tc::smem_desc_sw128(sbase + C::kOffKV, C::kSlab, 1024);
       uint32_t un = 0, q_phase = 0, p_phase = 0;   // a bit for each tile
-      int st = 0;                                  // the ring's stage and its phase
-      uint32_t kv_phase = 0;
-      int n = 0, nt = 0;
-      // the next unit that has keys; n = 0 at the end. False: a wait gave up.
+      struct Pos {                                 // a stage of the ring and its phase
+        int st;
+        uint32_t phase;
+      };
+      auto step = [](Pos& p) {                     // to the same operand of the next step
+        p.st += 2;
+        if (p.st >= NS) {
+          p.st -= NS;
+          p.phase ^= 1;
+        }
+      };
+      Pos kp = {0, 0}, vp = {1, 0};                // K and V take the stages in turn
+      int total = 0;                               // (step, tile) pairs of the unit
+      bool one = false;                            // one tile of rows
+      // the next unit that has keys; total = 0 at the end. False: a wait gave up.
       auto fetch = [&]() {
         while (true) {
           const int slot = un & 1;
@@ -507,81 +567,91 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&bars->info_empty[slot]);
           ++un;
           const bool stop = U.u < 0 || aborted(bars);
-          n = stop ? 0 : U.step1 - U.step0;
-          nt = U.ntok > half_tok ? 2 : 1;
-          if (stop || n > 0) return true;
+          one = U.ntok <= half_tok;
+          total = stop ? 0 : (U.step1 - U.step0) * (one ? 1 : 2);
+          if (stop || total > 0) return true;
         }
       };
-      auto full = [&]() { return mbar_wait(&bars->kv_full[st], kv_phase); };
-      auto next_stage = [&]() {
-        if (++st == NS) {
-          st = 0;
-          kv_phase ^= 1;
-        }
-      };
-      auto scores = [&](int t, int stage, bool last) {
-        const uint64_t dq = dq0 + ((t * C::kTile) >> 4), dk = dk0 + ((stage * C::kTile) >> 4);
+      auto full = [&](const Pos& p) { return mbar_wait(&bars->kv_full[p.st], p.phase); };
+      auto release = [&](const Pos& p) { tc::commit(&bars->kv_empty[p.st]); };
+      // S of tile t from Q tile q
+      auto scores = [&](int t, int q, const Pos& p) {
+        const uint64_t dq = dq0 + ((q * C::kTile) >> 4), dk = dk0 + ((p.st * C::kTile) >> 4);
+        tc::fence_after_sync();
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          const uint64_t off = ((ks >> 2) * C::kSlab + (ks & 3) * 32) >> 4;
+          const uint32_t off = ((ks >> 2) * C::kSlab + (ks & 3) * 32) >> 4;
           tc::mma_ss(tmem + 256 + 128 * t, dq + off, dk + off, idS, ks > 0);
         }
         tc::commit(&bars->s_full[t]);
-        if (last) tc::commit(&bars->q_empty[t]);   // Q is free after the unit's last scores
       };
+      // O of tile t += P V, P in two parts as the softmax hands them over
+      auto values = [&](int t, const Pos& p, bool first) {
+        const uint32_t s_tm = tmem + 256 + 128 * t, o_tm = tmem + 128 * t;
+        const uint32_t phase = (p_phase >> t) & 1;
+        p_phase ^= 1u << t;
+        const uint64_t dv = dv0 + ((p.st * C::kTile) >> 4);
+        if (!mbar_wait(&bars->p_ready[t][0], phase) || !full(p)) return false;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          tc::mma_ts(o_tm, s_tm + kk * 8, dv + ((kk * 2048) >> 4), idPV, !first || kk > 0);
+        if (!mbar_wait(&bars->p_ready[t][1], phase)) return false;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int kk = 4; kk < 8; ++kk)
+          tc::mma_ts(o_tm, s_tm + kk * 8, dv + ((kk * 2048) >> 4), idPV, true);
+        return true;
+      };
+      auto query = [&](int t) {
+        const uint32_t phase = (q_phase >> t) & 1;
+        q_phase ^= 1u << t;
+        return mbar_wait(&bars->q_full[t], phase);
+      };
+      // Pair i is step i / 2 of tile i % 2 (the K and V of a step are used twice) or, with one
+      // tile of rows, step i in tile i % 2 of tensor memory.
       bool ok = fetch();
-      while (ok && n > 0) {
-        if (!full()) { ok = false; break; }
-        for (int t = 0; t < nt && ok; ++t) {
-          ok = mbar_wait(&bars->q_full[t], (q_phase >> t) & 1);
+      while (ok && total > 0) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int q = one ? 0 : t;
+          if (t >= total || !ok) break;
+          if (t == 0 || !one) ok = query(q);
+          ok = ok && full(kp);
           if (!ok) break;
-          q_phase ^= 1u << t;
-          tc::fence_after_sync();
-          scores(t, st, n == 1);
+          scores(t, q, kp);
+          // Q is free after the unit's last scores
+          if (one ? t + 1 == total : t + 2 >= total) tc::commit(&bars->q_empty[q]);
+          if (one || t == 1) {
+            release(kp);
+            step(kp);
+          }
         }
-        if (!ok) break;
-        tc::commit(&bars->kv_empty[st]);
-        next_stage();
-        for (int j = 0; j < n && ok; ++j) {
-          const int sv = st;             // the stage of V (j); K (j + 1) is the next one
-          for (int t = 0; t < nt; ++t) {
-            const uint32_t s_tm = tmem + 256 + 128 * t, o_tm = tmem + 128 * t;
-            const uint32_t phase = (p_phase >> t) & 1;
-            p_phase ^= 1u << t;
-            if (!mbar_wait(&bars->p_ready[t][0], phase)) { ok = false; break; }
-            if (t == 0) {
-              ok = full();
-              next_stage();
-              if (!ok) break;
-            }
-            tc::fence_after_sync();
-            const uint64_t dv = dv0 + ((sv * C::kTile) >> 4);
+        for (int i0 = 0; i0 < total && ok; i0 += 2) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {   // keys 0-31 and 64-95
-              const int kk = i < 2 ? i : i + 2;
-              tc::mma_ts(o_tm, s_tm + kk * 8, dv + ((kk * 2048) >> 4), idPV, j > 0 || i > 0);
-            }
-            if (!mbar_wait(&bars->p_ready[t][1], phase)) { ok = false; break; }
-            tc::fence_after_sync();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int kk = i < 2 ? i + 2 : i + 4;
-              tc::mma_ts(o_tm, s_tm + kk * 8, dv + ((kk * 2048) >> 4), idPV, true);
-            }
-            const bool more = j + 1 < n;
+          for (int t = 0; t < 2; ++t) {
+            const int i = i0 + t, q = one ? 0 : t;
+            if (i >= total) break;
+            ok = values(t, vp, i0 == 0);
+            if (!ok) break;
+            const bool more = i + 2 < total;
             if (more) {
-              if (t == 0 && !full()) { ok = false; break; }
-              tc::fence_after_sync();
-              scores(t, st, j + 2 == n);
+              if (one || t == 0) ok = full(kp);
+              if (!ok) break;
+              scores(t, q, kp);
+              if (one ? i + 3 == total : i + 4 >= total) tc::commit(&bars->q_empty[q]);
             } else {
               tc::commit(&bars->o_full[t]);
             }
-          }
-          if (!ok) break;
-          tc::commit(&bars->kv_empty[sv]);
-          if (j + 1 < n) {
-            tc::commit(&bars->kv_empty[st]);
-            next_stage();
+            // the stages behind the scores: a commit takes its time, and the softmax waits for S
+            if (one || t == 1) {
+              release(vp);
+              step(vp);
+              if (more) {
+                release(kp);
+                step(kp);
+              }
+            }
           }
         }
         if (ok) ok = fetch();
@@ -593,49 +663,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------------ softmax of tile t
-    // Two threads a row, in warps w and w + 4 (a warp reaches the quarter w % 4 of tensor
-    // memory's rows): each has 64 of a step's 128 keys, and half of O's columns when it is
-    // rescaled or written. They swap row maxima (and, at the end, sums) through shared memory.
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-    const int t = warp >> 3, hf = (warp >> 2) & 1, quarter = warp & 3;
+    // Warp w has rows 32 (w % 4) .. + 31 of the tile (the quarter of tensor memory that it
+    // reaches), one a thread: row maxima and sums need no exchange.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int t = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_col = tmem + lane_addr + 256 + 128 * t;
-    const uint32_t o_col = tmem + lane_addr + 128 * t + hf * (D / 2);
-    const int tok = t * half_tok + row / a.G, hh = row % a.G;
-    const int warp_tok = t * half_tok + (quarter * 32) / a.G;   // of the warp's first row
     const float sc = a.scale_log2;
-    float* mine = &bars->swap[t][hf][row];
-    const float* theirs = &bars->swap[t][hf ^ 1][row];
-    uint64_t* pair = &bars->pair[t][quarter];
-    uint32_t un = 0, stepc = 0, oc = 0, swaps = 0;
-    // both threads of each row have written `mine`; theirs can be read
+    uint64_t* pair = &bars->pair[quarter];
+    // barrier phases, a bit each: 0-1 o_full of the tiles, 2 pair, 3 s_full, 4-5 units mod 4
+    uint32_t bits = 0;
+    // the warps of these rows in both tiles have come here
     auto meet = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(pair);
-      return warp_wait_all(pair, swaps++ & 1);
+      bits ^= 4;
+      return warp_wait_all(pair, ((bits >> 2) & 1) ^ 1);
     };
     while (true) {
-      const int slot = un & 1;
-      if (!warp_wait(&bars->info_full[slot], (un >> 1) & 1)) {
+      const int slot = (bits >> 4) & 1;
+      if (!warp_sleep_all(&bars->info_full[slot], (bits >> 5) & 1)) {
         if (lane == 0) set_abort(bars, a.status);
         break;
       }
-      const Unit U = bars->info[slot];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->info_empty[slot]);
-      ++un;
+      // Read again where it is needed and given back at the end: what lives across the step
+      // loop takes registers from the scores.
+      const volatile Unit& U = bars->info[slot];
+      bits = (bits & 15) | ((bits + 16) & 48);
       if (U.u < 0 || aborted(bars)) break;
-      if (t == 1 && U.ntok <= half_tok) continue;
-      const bool live = tok < U.ntok;
-      // the last key this row sees
-      const int last = !live ? -1 : a.causal ? min(U.pos0 + tok, U.len - 1) : U.len - 1;
       float m = -INFINITY;
       float2 l = make_float2(0.f, 0.f);
       bool ok = true;
-      const bool idle = warp_tok >= U.ntok;   // no row of this warp (and the other) exists
-      for (int step = U.step0; step < U.step1; ++step, ++stepc) {
-        if (!warp_sleep_all(&bars->s_full[t], stepc & 1)) { ok = false; break; }
+      // One tile of rows (twin): both tiles have the same rows and take the steps in turn.
+      int lim;                                  // columns 0 .. lim of the step are visible
+      bool idle;                                // no row of this warp exists
+      const int stride = U.ntok <= half_tok ? 2 : 1;
+      int left = U.step1 - U.step0 - (stride - 1) * t;
+      {
+        const int tok0 = stride == 2 ? 0 : t * half_tok, tok = tok0 + row / a.G;
+        // the last key this row sees
+        const int last = tok >= U.ntok ? -1 : a.causal ? min(U.pos0 + tok, U.len - 1) : U.len - 1;
+        lim = last - (U.step0 + (stride - 1) * t) * kStep;
+        idle = tok0 + (quarter * 32) / a.G >= U.ntok;
+      }
+      for (; left > 0; left -= stride, lim -= stride * kStep, bits ^= 8) {
+        if (!warp_wait_all(&bars->s_full[t], (bits >> 3) & 1)) { ok = false; break; }
         if (idle) {   // rows of P that nobody reads
           if (lane == 0) {
             mbar_arrive(&bars->p_ready[t][0]);
@@ -644,44 +717,40 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         tc::fence_after_sync();
-        uint32_t s[2][32];
-        tc::ld32(s_col + 64 * hf, s[0]);
-        tc::ld32(s_col + 64 * hf + 32, s[1]);
-        tc::wait_ld();
-        const int lim = last - step * kStep - 64 * hf;   // columns 0 .. lim are visible
-        if (lim < 63) {
+        uint32_t s[4][32];
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 4; ++i) tc::ld32(s_col + 32 * i, s[i]);
+        tc::wait_ld();
+        if (lim < kStep - 1) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int c = 0; c < 32; ++c)
               if (32 * i + c > lim) s[i][c] = 0xff800000u;
         }
         if (U.bad) {
-          const int blk = 2 * step + hf;
-          if (blk * kBlock < U.len && (block_row(a.k, U.b, U.g, blk, U.len, D) < 0 ||
-                                       block_row(a.v, U.b, U.g, blk, U.len, D) < 0)) {
+          for (int x = 0; x < 2; ++x) {
+            const int blk = 2 * (U.step1 - left) + x;
+            if (blk * kBlock < U.len && (block_row(a.k, U.b, U.g, blk, U.len, D) < 0 ||
+                                         block_row(a.v, U.b, U.g, blk, U.len, D) < 0)) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+              for (int i = 0; i < 4; ++i)
 #pragma unroll
-              for (int c = 0; c < 32; ++c) s[i][c] = 0xff800000u;
+                for (int c = 0; c < 32; ++c)
+                  if ((i >> 1) == x) s[i][c] = 0xff800000u;
+            }
           }
         }
         float mx[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t* v = &s[i >> 1][(i & 1) * 16];
-          mx[i] = max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+          mx[i] = max3(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]), __uint_as_float(s[i][2]));
 #pragma unroll
-          for (int c = 3; c < 15; c += 2)
-            mx[i] = max3(mx[i], __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-          mx[i] = fmaxf(mx[i], __uint_as_float(v[15]));
+          for (int c = 3; c < 31; c += 2)
+            mx[i] = max3(mx[i], __uint_as_float(s[i][c]), __uint_as_float(s[i][c + 1]));
+          mx[i] = fmaxf(mx[i], __uint_as_float(s[i][31]));
         }
-        const float part = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        *mine = part;
-        tc::fence_before_sync();   // S is in registers: the other thread may write P over it
-        if (!meet()) { ok = false; break; }
-        tc::fence_after_sync();
-        const float x = fmaxf(part, *theirs) * sc;
+        const float x = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
         const bool up = x > m + 8.0f;
         const float f = up ? ex2(m - x) : 1.0f;
         if (__any_sync(0xffffffffu, up)) {
@@ -690,33 +759,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             l.y *= f;
             m = x;
           }
-          if (step > U.step0) {
+          if (left < U.step1 - U.step0 - (stride - 1) * t) {
             // the tile's P V of the last step is done (its S was issued behind it)
 #pragma unroll 1
-            for (int c = 0; c < D / 2; c += 16) {
-              uint32_t ov[16];
-              tc::ld16(o_col + c, ov);
+            for (int c = 0; c < D; c += 32) {
+              uint32_t ov[32];
+              tc::ld32(s_col - 256 + c, ov);   // O of the tile
               tc::wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f);
-              tc::st16(o_col + c, ov);
+              for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f);
+              tc::st32(s_col - 256 + c, ov);
             }
           }
         }
         const float neg = m == -INFINITY ? 0.f : -m;
         const float2 neg2 = make_float2(neg, neg), sc2 = make_float2(sc, sc);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {   // the P V of the first 32 keys of each 64 starts early
-          uint32_t p[16];
+        for (int h = 0; h < 2; ++h) {   // the P V of the first 64 keys starts after the first half
 #pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const float2 v = __ffma2_rn(
-                make_float2(__uint_as_float(s[h][c]), __uint_as_float(s[h][c + 1])), sc2, neg2);
-            const float2 e = make_float2(ex2(v.x), ex2(v.y));
-            l = __fadd2_rn(l, e);
-            p[c / 2] = pack_bf16(e.x, e.y);
+          for (int i = 2 * h; i < 2 * h + 2; ++i) {
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              const float2 v = __ffma2_rn(
+                  make_float2(__uint_as_float(s[i][c]), __uint_as_float(s[i][c + 1])), sc2, neg2);
+              const float2 p = (c / 2) % kPolyOf >= kPolyOf - kPoly
+                                   ? exp2_poly(v) : make_float2(ex2(v.x), ex2(v.y));
+              l = __fadd2_rn(l, p);
+              s[i >> 1][(i & 1) * 16 + c / 2] = pack_bf16(p.x, p.y);
+            }
           }
-          tc::st16(s_col + 32 * hf + 16 * h, p);
+          tc::st32(s_col + 32 * h, s[h]);
           tc::wait_st();
           tc::fence_before_sync();
           __syncwarp();
@@ -727,47 +799,79 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) set_abort(bars, a.status);
         break;
       }
-      // ---- epilogue
+      // ---- epilogue: a thread writes its row or, with one tile of rows, half of it
       const bool empty = U.step1 <= U.step0;
-      if (idle) {
-        if (!empty) ++oc;
+      const bool one = U.ntok <= half_tok, twin = one && !empty;
+      const bool both = !one || U.step1 - U.step0 > 1;   // tile 1 had steps too
+      const int tok = (one ? 0 : t * half_tok) + row / a.G, hh = row % a.G;
+      const bool live = tok < U.ntok;
+      const uint32_t phases = bits;
+      if (!empty) bits ^= both ? 3u : 1u;
+      auto done = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->info_empty[slot]);
+      };
+      if (idle || (t == 1 && one && empty)) {
+        done();
         continue;
       }
-      *mine = l.x + l.y;
-      if (!meet() || (!empty && !warp_sleep_all(&bars->o_full[t], oc++ & 1))) {
+      float L = l.x + l.y;
+      if (twin) {
+        bars->swap[t][row] = make_float2(m, L);
+        ok = meet();
+      }
+      if (ok && !empty) {
+        if (twin || t == 0) ok = warp_sleep_all(&bars->o_full[0], phases & 1);
+        if (ok && both && (twin || t == 1)) ok = warp_sleep_all(&bars->o_full[1], (phases >> 1) & 1);
+      }
+      if (!ok) {
         if (lane == 0) set_abort(bars, a.status);
         break;
       }
       tc::fence_after_sync();
-      // the same order in both threads
-      const float L = hf ? *theirs + (l.x + l.y) : (l.x + l.y) + *theirs;
+      float f0 = 1.0f, f1 = 0.0f;     // weights of the two tiles' O
+      if (twin) {
+        const float2 x0 = bars->swap[0][row], x1 = bars->swap[1][row];
+        m = fmaxf(x0.x, x1.x);
+        const float base = m == -INFINITY ? 0.f : m;
+        f0 = ex2(x0.x - base);
+        f1 = ex2(x1.x - base);
+        L = x0.y * f0 + x1.y * f1;
+      }
       const bool part = U.nsplit > 1 || a.partial;
       const float inv = part ? 1.0f : L == 0.f ? 0.f : 1.0f / L;
+      f0 *= inv;
+      f1 *= inv;
       const int64_t at = (static_cast<int64_t>(U.row0) + tok) * a.Hq + U.g * a.G + hh;
       const int64_t pat = static_cast<int64_t>(U.split) * a.N * a.Hq + at;
+      const uint32_t o_first = tmem + lane_addr + (twin ? 0 : 128 * t);
+      const int col0 = twin ? t * (D / 2) : 0, col1 = twin ? col0 + D / 2 : D;
 #pragma unroll 1
-      for (int c = 0; c < D / 2; c += 32) {
-        uint32_t ov[32];
+      for (int c = col0; c < col1; c += 32) {
+        float v[32];
         if (empty) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) ov[i] = 0u;
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
         } else {
-          tc::ld32(o_col + c, ov);
+          uint32_t ov[32], ow[32];
+          tc::ld32(o_first + c, ov);
+          if (twin && both) tc::ld32(o_first + 128 + c, ow);
           tc::wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            v[i] = __uint_as_float(ov[i]) * f0;
+            if (twin && both) v[i] = fmaf(__uint_as_float(ow[i]), f1, v[i]);
+          }
         }
         if (live) {
-          const int cc = hf * (D / 2) + c;
-          float v[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(ov[i]) * inv;
           if (!part) {
-            uint4* ob = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + at * D + cc);
+            uint4* ob = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + at * D + c);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               ob[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
                                  pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
           }
-          float* of = part ? a.part_o + pat * D + cc : a.o_f32 != nullptr ? a.o_f32 + at * D + cc : nullptr;
+          float* of = part ? a.part_o + pat * D + c : a.o_f32 != nullptr ? a.o_f32 + at * D + c : nullptr;
           if (of != nullptr) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -775,15 +879,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (live && hf == 0) {
+      if (live && (!twin || t == 0)) {
         if (part)
           *reinterpret_cast<float2*>(a.part_ml + 2 * pat) = make_float2(m, L);
         else
           a.lse[at] = L == 0.f ? -INFINITY : (m + log2f(L)) * kLn2;
       }
       tc::fence_before_sync();
-      // the sums have been read before the next unit's first maxima are written
-      if (!meet()) {
+      const bool wait = twin;
+      done();
+      // both tiles' O and the swap have been read before the next unit writes them
+      if (wait && !meet()) {
         if (lane == 0) set_abort(bars, a.status);
         break;
       }
