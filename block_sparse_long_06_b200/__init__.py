@@ -359,7 +359,33 @@ class Tokens:
     r: int = 16
     block: int = BLOCK
 
+    def __post_init__(self):
+        self._kept = None
+
+    def __setattr__(self, name, value):
+        # the checked description is kept between calls until a field changes
+        object.__setattr__(self, name, value)
+        if name != "_kept":
+            object.__setattr__(self, "_kept", None)
+
+    def tensors(self):
+        rope = self.rope
+        return (self.cu_seqlens, self.seq_lens, self.positions, self.q_weight, self.k_weight,
+                None if rope is None else rope.steps)
+
     def c(self) -> CTokens:
+        kept, tensors = self._kept, self.tensors()
+        # a rope object may have been changed in place: its fields are part of the key
+        key = None if self.rope is None else (self.rope.steps, self.rope.interleaved, self.rope.factor)
+        if kept is None or (kept[1] is not key and (kept[1] is None or key is None or
+                                                    kept[1][0] is not key[0] or kept[1][1:] != key[1:])):
+            kept = self._kept = (self._describe(), key)
+        c = kept[0]
+        c.cu_seqlens, c.seq_lens, c.positions, c.q_weight, c.k_weight, c.rope_steps = [
+            None if t is None else t.data_ptr() for t in tensors]
+        return c
+
+    def _describe(self) -> CTokens:
         _want("cu_seqlens", self.cu_seqlens, torch.int32, (self.B + 1,))
         _want("seq_lens", self.seq_lens, torch.int32, (self.B,))
         _want("positions", self.positions, torch.int32, (self.N,))
@@ -369,13 +395,20 @@ class Tokens:
         if rope is not None:
             _want("rope.steps", rope.steps, torch.int64, (rope.steps.numel(),))
             dim = 2 * rope.steps.numel()
+        if len({t.get_device() for t in self.tensors() if t is not None}) > 1:
+            raise BsaError("Tokens: tensors on several devices")
         return CTokens(self.N, self.B, self.Hq, self.Hkv, self.d, self.r, self.block, self.T,
-                       _ptr(self.cu_seqlens), _ptr(self.seq_lens), _ptr(self.positions),
-                       None if rope is None else rope.steps.data_ptr(), dim,
-                       int(rope is not None and rope.interleaved),
+                       None, None, None, None, dim, int(rope is not None and rope.interleaved),
                        1.0 if rope is None else float(rope.factor), int(self.norm),
-                       float(self.eps), _ptr(self.q_weight), _ptr(self.k_weight),
-                       int(self.causal), float(self.attn_scale), int(self.q_stride))
+                       float(self.eps), None, None, int(self.causal), float(self.attn_scale),
+                       int(self.q_stride))
+
+    def device_index(self):
+        """The device of the description's tensors, -1 without any."""
+        for t in self.tensors():
+            if t is not None:
+                return t.get_device()
+        return -1
 
 
 _ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
@@ -385,55 +418,54 @@ def _want(name, t, dtype, shape):
     """Raise unless t is None or a contiguous device tensor of this type and shape."""
     if t is None:
         return
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise BsaError(f"{name}: contiguous {dtype} {tuple(shape)} wanted, got {t.dtype} "
                        f"{tuple(t.shape)} with strides {t.stride()}")
     if not t.is_cuda:
         raise BsaError(f"{name}: has to be on the GPU")
 
 
-def _rows(name, t, N, heads, width, dtype=None) -> CRows:
-    """Head rows [N, heads, width] of any token and head stride; None: no rows."""
+_NO_ROWS = CRows(None, 0, 0, 0)
+
+
+def _rows(name, t, N, heads, width, dev, out=False) -> CRows:
+    """Head rows [N, heads, width] on device `dev`, of any token and head stride; None: no
+    rows. Outputs are bfloat16."""
     if t is None:
-        return CRows(None, 0, 0, 0)
-    if t.dtype not in _ROW_TYPES or (dtype is not None and t.dtype != dtype):
-        raise BsaError(f"{name}: {dtype or 'bfloat16, float16 or float32'} wanted, got {t.dtype}")
-    if tuple(t.shape) != (N, heads, width) or (width > 1 and t.stride(2) != 1):
+        return _NO_ROWS
+    kind = _ROW_TYPES.get(t.dtype)
+    if kind is None or (out and kind != 0):
+        raise BsaError(f"{name}: {'bfloat16' if out else 'bfloat16, float16 or float32'} wanted, "
+                       f"got {t.dtype}")
+    if t.shape != (N, heads, width) or (stride := t.stride())[2] != 1:
         raise BsaError(f"{name}: [{N}, {heads}, {width}] with contiguous heads wanted, got "
                        f"{tuple(t.shape)} with strides {t.stride()}")
-    if not t.is_cuda:
-        raise BsaError(f"{name}: has to be on the GPU")
-    return CRows(t.data_ptr(), t.stride(0), t.stride(1), _ROW_TYPES[t.dtype])
+    if t.get_device() != dev or dev < 0:
+        raise BsaError(f"{name}: on {t.device}, wanted on the GPU and where the others are")
+    return CRows(t.data_ptr(), stride[0], stride[1], kind)
 
 
-def _same_device(*tensors):
-    """The device of the tensors that are not None; raises when they differ."""
-    dev = None
+def _check_device(dev, *tensors):
     for t in tensors:
-        if t is not None:
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise BsaError(f"tensors on {dev} and {t.device}")
-    return dev
+        if t is not None and t.get_device() != dev:
+            raise BsaError(f"a tensor on {t.device}, wanted on cuda:{dev} as the others")
 
 
-class _on:
-    """Make `device` the current one for a launch (streams and kernels belong to it)."""
+def _raw_stream(stream, dev) -> int:
+    """The stream's handle; None: the current stream of device `dev`."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
-    def __init__(self, device):
-        self.device = device
-        self.before = -1
 
-    def __enter__(self):
-        now = torch.cuda.current_device()
-        if self.device.index != now:
-            self.before = now
-            torch.cuda.set_device(self.device)
-
-    def __exit__(self, *exc):
-        if self.before >= 0:
-            torch.cuda.set_device(self.before)
+def _launch(fn, what, dev, *args):
+    """Call an entry point with `dev` as the current device (kernels and streams belong to
+    it) and raise on a status."""
+    if torch.cuda.current_device() == dev:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args)
+    if status != BSA_OK:
+        _check(status, what)
 
 
 # ------------------------------------------------------------------ the C entry points
@@ -514,25 +546,20 @@ def bsa_pbs_permute(prob: Problem, q, k: Cache, v: Cache, k_idx: Cache, k_perm, 
            "bsa_pbs_permute")
 
 
-def _token_tensors(tok: Tokens):
-    return (tok.cu_seqlens, tok.seq_lens, tok.positions, tok.q_weight, tok.k_weight,
-            None if tok.rope is None else tok.rope.steps)
-
-
 def bsa_norm_rope(tok: Tokens, q, q_out, k=None, k_out=None, dev_status=None, stream=None):
     """Norm (tok.norm) and rotate (tok.rope) the heads of q [N, Hq, d] into q_out and of
     k [N, Hkv, d] into k_out (bf16; either pair may be None, outputs may be the inputs)."""
-    if (q is None) != (q_out is None) or (k is None) != (k_out is None):
-        raise BsaError("bsa_norm_rope: q and q_out, k and k_out come together")
-    dev = _same_device(q, q_out, k, k_out, dev_status, *_token_tensors(tok))
-    if dev is None:
-        raise BsaError("bsa_norm_rope: neither q nor k")
-    N, bf16 = tok.N, torch.bfloat16
-    args = (_rows("q", q, N, tok.Hq, tok.d), _rows("q_out", q_out, N, tok.Hq, tok.d, bf16),
-            _rows("k", k, N, tok.Hkv, tok.d), _rows("k_out", k_out, N, tok.Hkv, tok.d, bf16))
-    with _on(dev):
-        _check(load_library().bsa_norm_rope(ctypes.byref(tok.c()), *args, _ptr(dev_status),
-                                            _stream(stream)), "bsa_norm_rope")
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None) or q is k is None:
+        raise BsaError("bsa_norm_rope: q and q_out, k and k_out come together, one pair at least")
+    dev = (k if q is None else q).get_device()
+    N, d, c = tok.N, tok.d, tok.c()
+    if tok.device_index() not in (-1, dev):
+        raise BsaError("bsa_norm_rope: the description's tensors are on another device")
+    _check_device(dev, dev_status)
+    _launch(load_library().bsa_norm_rope, "bsa_norm_rope", dev, c,
+            _rows("q", q, N, tok.Hq, d, dev), _rows("q_out", q_out, N, tok.Hq, d, dev, True),
+            _rows("k", k, N, tok.Hkv, d, dev), _rows("k_out", k_out, N, tok.Hkv, d, dev, True),
+            None if dev_status is None else dev_status.data_ptr(), _raw_stream(stream, dev))
 
 
 def bsa_append_kv(tok: Tokens, k, v, k_cache: Cache, v_cache: Cache, k_idx=None,
@@ -543,17 +570,20 @@ def bsa_append_kv(tok: Tokens, k, v, k_cache: Cache, v_cache: Cache, k_idx=None,
     rotated into q_out by the same launch."""
     if (q is None) != (q_out is None) or (k_idx is None) != (kidx_cache is None):
         raise BsaError("bsa_append_kv: q and q_out, k_idx and kidx_cache come together")
-    caches = [c for c in (k_cache, v_cache, kidx_cache) if c is not None]
-    dev = _same_device(k, v, k_idx, q, q_out, dev_status, *_token_tensors(tok),
-                       *(c.tensor for c in caches), *(c.page_table for c in caches))
-    N, d = tok.N, tok.d
-    args = (_rows("k", k, N, tok.Hkv, d), _rows("v", v, N, tok.Hkv, d),
-            _rows("k_idx", k_idx, N, tok.Hkv, tok.r), k_cache.c(), v_cache.c(),
-            CCache() if kidx_cache is None else kidx_cache.c(), _rows("q", q, N, tok.Hq, d),
-            _rows("q_out", q_out, N, tok.Hq, d, torch.bfloat16))
-    with _on(dev):
-        _check(load_library().bsa_append_kv(ctypes.byref(tok.c()), *args, _ptr(dev_status),
-                                            _stream(stream)), "bsa_append_kv")
+    dev = k.get_device()
+    N, d, H, c = tok.N, tok.d, tok.Hkv, tok.c()
+    if tok.device_index() not in (-1, dev):
+        raise BsaError("bsa_append_kv: the description's tensors are on another device")
+    _check_device(dev, dev_status, k_cache.tensor, k_cache.page_table, v_cache.tensor,
+                  v_cache.page_table)
+    if kidx_cache is not None:
+        _check_device(dev, kidx_cache.tensor, kidx_cache.page_table)
+    _launch(load_library().bsa_append_kv, "bsa_append_kv", dev, c,
+            _rows("k", k, N, H, d, dev), _rows("v", v, N, H, d, dev),
+            _rows("k_idx", k_idx, N, H, tok.r, dev), k_cache.c(), v_cache.c(),
+            CCache() if kidx_cache is None else kidx_cache.c(),
+            _rows("q", q, N, tok.Hq, d, dev), _rows("q_out", q_out, N, tok.Hq, d, dev, True),
+            None if dev_status is None else dev_status.data_ptr(), _raw_stream(stream, dev))
 
 
 def bsa_packed_workspace_size(tok: Tokens, op: int) -> int:
@@ -564,31 +594,37 @@ def bsa_packed_workspace_size(tok: Tokens, op: int) -> int:
 
 
 def _packed_call(name, tok, q, k, v, own, o, lse, o_f32, workspace, dev_status, stream):
-    dev = _same_device(q, k.tensor, v.tensor, k.page_table, v.page_table, *own, o, lse, o_f32,
-                       workspace, dev_status, *_token_tensors(tok))
+    dev = q.get_device()
     N, Hq, d = tok.N, tok.Hq, tok.d
-    if q.dtype != torch.bfloat16 or tuple(q.shape) != (N, Hq, d) or not q.is_cuda or (
-            N > 0 and (q.stride(2) != 1 or q.stride(1) != d)):
+    stride = q.stride()
+    if q.dtype != torch.bfloat16 or q.shape != (N, Hq, d) or dev < 0 or (
+            N > 0 and (stride[2] != 1 or stride[1] != d)):
         raise BsaError(f"{name}: q has to be bfloat16 [{N}, {Hq}, {d}] on the GPU, a token's "
                        f"heads side by side, got {q.dtype} {tuple(q.shape)} {q.stride()}")
     c = tok.c()
-    if N > 1:
-        if tok.q_stride not in (0, q.stride(0)):
-            raise BsaError(f"{name}: q_stride {tok.q_stride}, but q has {q.stride(0)}")
-        c.q_stride = q.stride(0)
+    if tok.device_index() not in (-1, dev):
+        raise BsaError(f"{name}: the description's tensors are on another device")
+    _check_device(dev, k.tensor, k.page_table, v.tensor, v.page_table, o, lse, o_f32, workspace,
+                  dev_status, *own)
     _want("o", o, torch.bfloat16, (N, Hq, d))
     _want("lse", lse, torch.float32, (N, Hq))
     _want("o_f32", o_f32, torch.float32, (N, Hq, d))
-    ptrs = [_ptr(q), k.c(), v.c()]
-    if name == "bsa_decode_shared":
+    if N > 1:
+        if tok.q_stride not in (0, stride[0]):
+            raise BsaError(f"{name}: q_stride {tok.q_stride}, but q has {stride[0]}")
+        if stride[0] != Hq * d:
+            c = CTokens.from_buffer_copy(c)
+            c.q_stride = stride[0]
+    args = [c, q.data_ptr(), k.c(), v.c()]
+    if own:
         _want("o_own", own[0], torch.float32, (N, Hq, d))
         _want("lse_own", own[1], torch.float32, (N, Hq))
-        ptrs += [_ptr(own[0]), _ptr(own[1])]
-    with _on(dev):
-        _check(getattr(load_library(), name)(
-            ctypes.byref(c), *ptrs, _ptr(o), _ptr(lse), _ptr(o_f32), _ptr(workspace),
+        args += [None if t is None else t.data_ptr() for t in own]
+    _launch(getattr(load_library(), name), name, dev, *args, o.data_ptr(), lse.data_ptr(),
+            None if o_f32 is None else o_f32.data_ptr(),
+            None if workspace is None else workspace.data_ptr(),
             0 if workspace is None else workspace.numel() * workspace.element_size(),
-            _ptr(dev_status), _stream(stream)), name)
+            None if dev_status is None else dev_status.data_ptr(), _raw_stream(stream, dev))
 
 
 def bsa_attend_packed(tok: Tokens, q, k: Cache, v: Cache, o, lse, o_f32, workspace,
