@@ -290,6 +290,7 @@ PackedWorkspace packed_workspace(const bsa_tokens_t* t, bool shared, int num_sms
   const int64_t want = (4ll * num_sms + least * t->Hkv - 1) / (least * t->Hkv);
   const int64_t steps = (t->T + 127) / 128;
   w.smax = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, 64), steps)));
+  if (steps <= 2) w.smax = 1;   // a split has the cost of 4 steps of one tile at least
   w.max_entries = static_cast<int>((least + std::min<int64_t>(rows, t->B)) * w.smax);
   w.offs = 256;
   w.entries = w.offs + align256((static_cast<size_t>(t->B) + 1) * sizeof(int32_t));

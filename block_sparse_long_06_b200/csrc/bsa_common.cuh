@@ -208,6 +208,10 @@ BSA_DEVFN float2 unpack_bf16(uint32_t x) {
 // the stream reads or writes; the code before it only sets up shared memory.
 BSA_DEVFN void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Let the kernel launched behind this one (launch_pdl) start its own setup already; its
+// grid_dependency_wait still waits for this whole grid.
+BSA_DEVFN void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Value of an E4M3 (FP8, bias 7, with subnormals) code; 0x7F (NaN) is never produced
 // by the index-key quantiser.
 BSA_DEVFN float e4m3_value(uint32_t code) {

@@ -26,8 +26,7 @@
 //    bf16, so no value range is lost.
 //  * Few rows over many keys: the plan kernel (one block) cuts units into splits of the key
 //    axis, until the SMs are filled; each writes its O, m and l in fp32 and the merge kernel
-//    joins them. Units are handed out longest first, one kv head after the other, so the
-//    SMs share one head's keys through L2 at a time.
+//    joins them. Units are handed out longest first.
 //  * Rows of V behind a sequence's end are whatever the page held before: a patch warp
 //    zeroes them in shared memory in the step that has the end (0 * NaN is NaN), before the
 //    step is handed to the tensor cores. K there may be anything: its scores are replaced.
@@ -48,8 +47,8 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kStep = 128;             // keys a step
 constexpr int kMaxStages = 10;
 constexpr int kPlanThreads = 1024;
-constexpr int kBuckets = 512, kPlanTiles = 1024;
-constexpr float kUnitCost = 4.f;       // of a unit besides its steps, in steps of one tile
+constexpr int kBuckets = 512, kPlanTiles = 1024, kPlanSeqs = 1024;
+constexpr float kUnitCost = 4.f, kMergeCost = 6.f, kRowsCost = 64.f;   // in steps of one tile
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -169,36 +168,19 @@ BSA_DEVFN int seq_len(const PackedArgs& a, int b) {
   return a.seq_lens != nullptr ? max(0, min(a.seq_lens[b], a.T)) : a.T;
 }
 
-// Tile `t` of all sequences' tiles, in order; offs[b] is the first tile of sequence b.
-BSA_DEVFN Tile tile_of(const PackedArgs& a, int t) {
-  int lo = 0, hi = a.B - 1;            // the last b with offs[b] <= t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.offs[mid] <= t) lo = mid; else hi = mid - 1;
-  }
-  const int per = packed_unit_tokens(a.G);
-  const int first = seq_first(a, lo), count = seq_first(a, lo + 1) - first;
-  const int i = (t - a.offs[lo]) * per;
-  Tile r;
-  r.b = lo;
-  r.row0 = first + i;
-  r.ntok = min(per, count - i);
-  r.len = seq_len(a, lo);
-  r.pos0 = r.len - count + i;
-  const int end = a.causal ? max(0, min(r.len, r.pos0 + r.ntok)) : r.len;
-  r.steps = (end + kStep - 1) / kStep;
-  return r;
-}
-
 // One block: lists the units (tile, split of its keys) of one kv head, longest first.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) {
   __shared__ int warp_sum[32];
   __shared__ int carry, bad, longest;
   __shared__ unsigned long long work, best;   // best: (time, candidate)
   __shared__ int bucket[kBuckets], costs[kPlanTiles];
+  // first row, length and first tile of each sequence, for up to kPlanSeqs of them
+  __shared__ int s_first[kPlanSeqs + 1], s_len[kPlanSeqs], s_offs[kPlanSeqs];
+  grid_launch_dependents();            // the attention kernel sets up meanwhile, and waits for this one
   grid_dependency_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = packed_unit_tokens(a.G);
+  const int per = packed_unit_tokens(a.G), half = per / 2;
+  const bool small = a.B <= kPlanSeqs;
   if (tid == 0) {
     carry = 0;
     bad = 0;
@@ -214,13 +196,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) 
     int tiles = 0;
     if (b < a.B) {
       const int first = seq_first(a, b), last = seq_first(a, b + 1);
+      const int len = a.seq_lens != nullptr ? a.seq_lens[b] : a.T;
       if (first < 0 || last < first || last > a.N || (b == 0 && first != 0)) {
         bad = 1;
       } else {
         tiles = (last - first + per - 1) / per;
-        const int len = a.seq_lens != nullptr ? a.seq_lens[b] : a.T;
         if (len < 0 || len > a.T || (a.causal && len < last - first))
           report(a.status, BSA_DEV_BAD_LENGTH);
+      }
+      if (small) {
+        s_first[b] = first;
+        if (b == a.B - 1) s_first[a.B] = last;
+        s_len[b] = max(0, min(len, a.T));
       }
     }
     int x = tiles;
@@ -233,7 +220,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) 
     __syncthreads();
     int before = carry;
     for (int w = 0; w < warp; ++w) before += warp_sum[w];
-    if (b < a.B) a.offs[b] = before + x - tiles;
+    if (b < a.B) {
+      if (small) s_offs[b] = before + x - tiles; else a.offs[b] = before + x - tiles;
+    }
     __syncthreads();
     if (tid == kPlanThreads - 1) carry = before + x;
     __syncthreads();
@@ -241,14 +230,36 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) 
   const bool refuse = bad != 0;
   const int ntiles = refuse ? 0 : carry;
   if (refuse && tid == 0) report(a.status, BSA_DEV_BAD_LENGTH);
+  // tile t of all sequences' tiles, in order
+  auto tile_of = [&](int t) {
+    int lo = 0, hi = a.B - 1;          // the last b whose first tile is at most t
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((small ? s_offs[mid] : a.offs[mid]) <= t) lo = mid; else hi = mid - 1;
+    }
+    const int first = small ? s_first[lo] : seq_first(a, lo);
+    const int count = (small ? s_first[lo + 1] : seq_first(a, lo + 1)) - first;
+    const int i = (t - (small ? s_offs[lo] : a.offs[lo])) * per;
+    Tile r;
+    r.b = lo;
+    r.row0 = first + i;
+    r.ntok = min(per, count - i);
+    r.len = small ? s_len[lo] : seq_len(a, lo);
+    r.pos0 = r.len - count + i;
+    const int end = a.causal ? max(0, min(r.len, r.pos0 + r.ntok)) : r.len;
+    r.steps = (end + kStep - 1) / kStep;
+    return r;
+  };
+  Tile own;                            // this thread's first tile: one is all there is, mostly
+  if (tid < ntiles) own = tile_of(tid);
+  auto tile = [&](int t) { return t == tid ? own : tile_of(t); };
   // cost of all tiles and of the costliest: a step of two 128-row tiles costs twice a step of one
-  const int half = per / 2;
   auto cost_of = [&](const Tile& x) { return x.ntok > half ? 2 * x.steps : x.steps; };
   unsigned long long sum = 0;
   int top = 0;
   for (int t = tid; t < ntiles; t += kPlanThreads) {
-    const int c = cost_of(tile_of(a, t));
-    if (t < kPlanTiles) costs[t] = c;
+    const int c = cost_of(tile(t));
+    if (t < kPlanTiles) costs[t] = c | (tile(t).ntok << 20);
     sum += c;
     top = max(top, c);
   }
@@ -264,22 +275,29 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) 
   // costliest (started first) is no more than an SM's share. Else the cost that a unit may have
   // is searched, a warp for each candidate: the time is the costliest unit's where every unit
   // has an SM of its own, and otherwise an SM's share of all costs and half of the costliest.
-  // A unit costs kUnitCost besides its steps (start, epilogue, its part of the merge).
+  // A unit costs kUnitCost besides its steps, a merge kMergeCost and as much as a step for each
+  // kRowsCost partial rows that are written and read again.
   const float share = static_cast<float>(work) * a.Hkv / a.num_sms;
   int limit = 1 << 30;
   if (a.smax > 1 && ntiles <= kPlanTiles &&
       !(static_cast<float>(longest) <= share && static_cast<long long>(ntiles) * a.Hkv >= 3ll * a.num_sms)) {
     const int cand = warp == 0 ? 1 << 30 : max(4, static_cast<int>(share * (0.1f + 0.06f * warp)) + 1);
-    int units = 0, piece = 0;
+    int units = 0, piece = 0, parts = 0;        // parts: rows that go through the merge
     for (int t = lane; t < ntiles; t += 32) {
-      const int k = max(1, min(a.smax, (costs[t] + cand - 1) / cand));
+      const int c = costs[t] & 0xfffff;
+      const int k = max(1, min(a.smax, (c + cand - 1) / cand));
       units += k;
-      piece = max(piece, (costs[t] + k - 1) / k);
+      piece = max(piece, (c + k - 1) / k);
+      if (k > 1 || a.partial) parts += k * (costs[t] >> 20) * a.G;
     }
     units = __reduce_add_sync(0xffffffffu, units) * a.Hkv;
+    parts = __reduce_add_sync(0xffffffffu, parts);
     piece = __reduce_max_sync(0xffffffffu, piece);
     const float unit = piece + kUnitCost;
-    const float time = units <= a.num_sms ? unit : share + units * kUnitCost / a.num_sms + 0.5f * unit;
+    const float merge = (parts > 0 && !a.partial ? kMergeCost : 0.f) +
+                        static_cast<float>(parts) * a.Hkv / (kRowsCost * a.num_sms);
+    const float time =
+        merge + (units <= a.num_sms ? unit : share + units * kUnitCost / a.num_sms + 0.5f * unit);
     if (lane == 0) atomicMin(&best, (static_cast<unsigned long long>(__float_as_uint(time)) << 32) |
                                         static_cast<unsigned>(cand));
     __syncthreads();
@@ -294,7 +312,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) 
   };
   bool any = false;
   for (int t = tid; t < ntiles; t += kPlanThreads) {
-    const Tile x = tile_of(a, t);
+    const Tile x = tile(t);
     const int n = splits_of(x);
     any |= n > 1;
     atomicAdd(&bucket[bucket_of(x, n)], n);
@@ -319,7 +337,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) 
   }
   __syncthreads();
   for (int t = tid; t < ntiles; t += kPlanThreads) {
-    const Tile y = tile_of(a, t);
+    const Tile y = tile(t);
     const int n = splits_of(y);
     const int at = atomicAdd(&bucket[bucket_of(y, n)], n);
     for (int s = 0; s < n; ++s) {
@@ -384,34 +402,89 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = bars->tmem_base;
+  if (warp == kWarpLoad && lane == 0) {
+    prefetch_tensormap(&tmq);
+    prefetch_tensormap(&tmk);
+    prefetch_tensormap(&tmv);
+  }
+  grid_launch_dependents();            // the merge kernel may be set up, and waits for this one
   grid_dependency_wait();
 
   if (warp >= kSoftmaxWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kWarpLoad) {
       // ---------------------------------------------------------------- Q / K / V
-      const int entries = a.head[0];
-      const int units = entries * a.Hkv;
       uint32_t un = 0, kc = 0, qc[2] = {0, 0};
-      bool ok = true;
+      bool ok = true, taken = false;
+      int entries = 0;
       while (ok) {
         const int slot = un & 1;
         Unit U = {-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-        int u = -1;
-        if (lane == 0) u = atomicAdd(&a.head[1], 1);
-        u = __shfl_sync(0xffffffffu, u, 0);
-        if (u < units) {
-          const int g = u / entries, e = u - g * entries;
-          const int4 e0 = a.entries[2 * e], e1 = a.entries[2 * e + 1];
-          U = {u, e0.x, g, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w & 0xffff, e1.w >> 16, 0};
-          // blocks with a bad page or beyond the cache: found before the unit starts
-          const int nblk = (U.len + kBlock - 1) / kBlock;
+        int u = blockIdx.x;            // the first unit; the others come from the counter
+        if (taken) {
+          if (lane == 0) u = static_cast<int>(gridDim.x) + atomicAdd(&a.head[1], 1);
+          u = __shfl_sync(0xffffffffu, u, 0);
+        }
+        // The heads of an entry are neighbours: the longest units of all heads start first
+        // (prompts of 2K and 4K: 53 and 146 us, 69 and 168 with one head after the other), and
+        // an entry is read beside the number of entries. Without the causal limit units are
+        // alike, and one head comes after the other where they do not all run at once, so that
+        // the units at work share its keys through L2 (200 rows behind three prefixes of up to
+        // 64K: 399 us, 437 with the heads as neighbours).
+        int e = min(u / a.Hkv, a.max_entries - 1), g = u % a.Hkv;
+        int4 e0 = a.entries[2 * e], e1 = a.entries[2 * e + 1];
+        if (!taken) entries = a.head[0];
+        taken = true;
+        const int units = entries * a.Hkv;
+        if (!a.causal && units > static_cast<int>(gridDim.x) && u < units) {
+          g = u / entries;
+          e = u - g * entries;
+          e0 = a.entries[2 * e];
+          e1 = a.entries[2 * e + 1];
+        }
+        int rk = -1, rv = -1, nblk = 0;
+        // the cache rows of the unit's blocks from `first`, one a lane: -1 behind the end, and
+        // for a bad block
+        auto look_up = [&](int first) {
+          const int blk = first + lane;
+          rk = rv = -1;
           bool bad = false;
-          for (int blk = 2 * U.step0 + lane; blk < min(2 * U.step1, nblk); blk += 32)
-            bad |= block_row(a.k, U.b, g, blk, U.len, D) < 0 ||
-                   block_row(a.v, U.b, g, blk, U.len, D) < 0;
-          U.bad = __any_sync(0xffffffffu, bad) ? 1 : 0;
-          if (U.bad && lane == 0) report(a.status, BSA_DEV_BAD_PAGE);
+          if (blk < nblk && blk < 2 * U.step1) {
+            rk = static_cast<int>(block_row(a.k, U.b, U.g, blk, U.len, D));
+            rv = static_cast<int>(block_row(a.v, U.b, U.g, blk, U.len, D));
+            bad = rk < 0 || rv < 0;
+            if (bad) rk = rv = -1;
+          }
+          return __any_sync(0xffffffffu, bad);
+        };
+        if (u < units) {
+          U = {u, e0.x, g, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w & 0xffff, e1.w >> 16, 0};
+          nblk = (U.len + kBlock - 1) / kBlock;
+          if (U.step1 > U.step0) {
+            const int ntiles = U.ntok > half_tok ? 2 : 1;
+            if (lane == 0) {
+              for (int t = 0; t < ntiles && ok; ++t) {
+                if (!mbar_wait_sleep(&bars->q_empty[t], (qc[t] & 1) ^ 1)) { ok = false; break; }
+                mbar_arrive_expect_tx(&bars->q_full[t], C::kTile);
+                for (int x = 0; x < C::kHalves; ++x)
+                  tma_load_3d(smem + t * C::kTile + x * C::kSlab, &tmq, x * 64, U.g * a.G,
+                              U.row0 + t * half_tok, &bars->q_full[t]);
+                ++qc[t];
+              }
+            }
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            if (!ok) break;
+          }
+          // blocks with a bad page or beyond the cache are found before the unit starts
+          bool bad = look_up(2 * U.step0);
+          for (int first = 2 * U.step0 + 32; first < min(2 * U.step1, nblk) && !bad; first += 32) {
+            const int keep_k = rk, keep_v = rv;
+            bad = look_up(first);
+            rk = keep_k;
+            rv = keep_v;
+          }
+          U.bad = bad ? 1 : 0;
+          if (bad && lane == 0) report(a.status, BSA_DEV_BAD_PAGE);
         }
         if (lane == 0) {
           if (!mbar_wait_sleep(&bars->info_empty[slot], ((un >> 1) & 1) ^ 1)) {
@@ -424,29 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         if (!ok || U.u < 0 || aborted(bars)) break;
         ++un;
-        if (U.step1 <= U.step0) continue;
-        const int ntiles = U.ntok > half_tok ? 2 : 1;
-        if (lane == 0) {
-          for (int t = 0; t < ntiles && ok; ++t) {
-            if (!mbar_wait_sleep(&bars->q_empty[t], (qc[t] & 1) ^ 1)) { ok = false; break; }
-            mbar_arrive_expect_tx(&bars->q_full[t], C::kTile);
-            for (int x = 0; x < C::kHalves; ++x)
-              tma_load_3d(smem + t * C::kTile + x * C::kSlab, &tmq, x * 64, U.g * a.G,
-                          U.row0 + t * half_tok, &bars->q_full[t]);
-            ++qc[t];
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        const int nblk = (U.len + kBlock - 1) / kBlock;
         for (int s0 = U.step0; s0 < U.step1 && ok; s0 += 16) {
-          // the blocks of 16 steps, one a lane
-          const int blk = 2 * s0 + lane;
-          int rk = -1, rv = -1;
-          if (blk < nblk && blk < 2 * U.step1) {
-            rk = static_cast<int>(block_row(a.k, U.b, U.g, blk, U.len, D));
-            rv = static_cast<int>(block_row(a.v, U.b, U.g, blk, U.len, D));
-            if (rk < 0 || rv < 0) rk = rv = -1;
-          }
+          if (s0 > U.step0) look_up(2 * s0);
           const int n_here = min(16, U.step1 - s0);
           for (int q = 0; q < n_here; ++q) {
             const int k0 = __shfl_sync(0xffffffffu, rk, 2 * q), k1 = __shfl_sync(0xffffffffu, rk, 2 * q + 1);
@@ -906,13 +958,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------------------- merge
 // One warp per (row, head): joins the splits' (o, m, l) and, with o_own, what the row's own
-// tokens gave.
+// tokens gave. The lanes read 32 splits' (m, l) at once; the partial rows are read in 16-byte
+// loads, eight in flight, by 32 or, at d = 64, two times 16 lanes, and added in a fixed order.
 template <int D>
 __global__ void __launch_bounds__(256) packed_merge_kernel(const PackedArgs a) {
   grid_dependency_wait();
   if (a.head[2] == 0) return;
-  constexpr int kPer = D / 32;
-  const int lane = threadIdx.x & 31;
+  constexpr int kLanes = D / 4, kRows = 32 / kLanes;   // lanes a partial row, rows at a time
+  const int lane = threadIdx.x & 31, sub = lane % kLanes, slot = lane / kLanes;
   const int64_t at = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   if (at >= static_cast<int64_t>(a.N) * a.Hq) return;
   const int n = a.row_splits[at / a.Hq];
@@ -925,9 +978,7 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(const PackedArgs a) {
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const float base = M == -INFINITY ? 0.f : M;
   float L = 0.f;
-  float2 o[kPer / 2];
-#pragma unroll
-  for (int q = 0; q < kPer / 2; ++q) o[q] = make_float2(0.f, 0.f);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int c = 0; c < n; c += 32) {
     float f = 0.f;
     if (c + lane < n) {
@@ -936,37 +987,59 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(const PackedArgs a) {
       L += ml.y * f;
     }
     const int here = min(32, n - c);
-#pragma unroll 4
-    for (int j = 0; j < here; ++j) {
-      const float fj = __shfl_sync(0xffffffffu, f, j);
-      const float2* po = reinterpret_cast<const float2*>(a.part_o + ((c + j) * rows + at) * D);
+    const float* from = a.part_o + ((c + slot) * rows + at) * D + sub * 4;
+    int j0 = 0;
+    for (; j0 + 8 * kRows <= here; j0 += 8 * kRows) {
+      float4 v[8];
 #pragma unroll
-      for (int q = 0; q < kPer / 2; ++q) {
-        const float2 v = po[lane + 32 * q];
-        o[q].x = fmaf(v.x, fj, o[q].x);
-        o[q].y = fmaf(v.y, fj, o[q].y);
+      for (int u = 0; u < 8; ++u)
+        v[u] = *reinterpret_cast<const float4*>(from + (j0 + u * kRows) * rows * D);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float fj = __shfl_sync(0xffffffffu, f, j0 + u * kRows + slot);
+        o.x = fmaf(v[u].x, fj, o.x);
+        o.y = fmaf(v[u].y, fj, o.y);
+        o.z = fmaf(v[u].z, fj, o.z);
+        o.w = fmaf(v[u].w, fj, o.w);
+      }
+    }
+#pragma unroll 4
+    for (; j0 < here; j0 += kRows) {
+      const int j = j0 + slot;                   // at d = 64 the last may be one too many
+      float fj = __shfl_sync(0xffffffffu, f, min(j, 31));
+      if (j < here) {
+        const float4 v = *reinterpret_cast<const float4*>(from + j0 * rows * D);
+        o.x = fmaf(v.x, fj, o.x);
+        o.y = fmaf(v.y, fj, o.y);
+        o.z = fmaf(v.z, fj, o.z);
+        o.w = fmaf(v.w, fj, o.w);
       }
     }
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+  if constexpr (kRows == 2) {
+    o.x += __shfl_xor_sync(0xffffffffu, o.x, 16);
+    o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
+    o.z += __shfl_xor_sync(0xffffffffu, o.z, 16);
+    o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
+  }
   if (own != -INFINITY) {     // o_own is normalised: a part with l = 1 at its log-sum
     const float f = ex2(own - base);
     L += f;
-    const float2* po = reinterpret_cast<const float2*>(a.o_own + at * D);
-#pragma unroll
-    for (int q = 0; q < kPer / 2; ++q) {
-      const float2 v = po[lane + 32 * q];
-      o[q].x = fmaf(v.x, f, o[q].x);
-      o[q].y = fmaf(v.y, f, o[q].y);
-    }
+    const float4 v = *reinterpret_cast<const float4*>(a.o_own + at * D + sub * 4);
+    o.x = fmaf(v.x, f, o.x);
+    o.y = fmaf(v.y, f, o.y);
+    o.z = fmaf(v.z, f, o.z);
+    o.w = fmaf(v.w, f, o.w);
   }
   const float inv = L == 0.f ? 0.f : 1.0f / L;
-#pragma unroll
-  for (int q = 0; q < kPer / 2; ++q) {
-    const float2 v = make_float2(o[q].x * inv, o[q].y * inv);
-    reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.o) + at * D)[lane + 32 * q] = pack_bf16(v.x, v.y);
-    if (a.o_f32 != nullptr) reinterpret_cast<float2*>(a.o_f32 + at * D)[lane + 32 * q] = v;
+  o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  __syncwarp();               // o_f32 may be o_own: every lane has read it
+  if (slot == 0) {
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + at * D + sub * 4) =
+        make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+    if (a.o_f32 != nullptr) *reinterpret_cast<float4*>(a.o_f32 + at * D + sub * 4) = o;
   }
   if (lane == 0) a.lse[at] = L == 0.f ? -INFINITY : (base + log2f(L)) * kLn2;
 }
