@@ -320,6 +320,18 @@ bool make_q_map(CUtensorMap* m, const void* q, const bsa_tokens_t* t, int64_t st
   return r == CUDA_SUCCESS;
 }
 
+// Whether every block that a valid page number (or a token below T) leads to lies whole inside
+// the extent.
+bool inside_extent(const bsa_cache_t& c, const bsa_tokens_t* t) {
+  const int64_t blocks = c.page_table != nullptr ? c.num_pages : nblocks(t->T);
+  if (blocks == 0) return true;
+  // in 128 bits: the strides are the caller's
+  const __int128 last = static_cast<__int128>(t->B - 1) * c.seq_stride +
+                        static_cast<__int128>(blocks - 1) * c.block_stride +
+                        static_cast<__int128>(t->Hkv - 1) * c.head_stride + 64ll * t->d;
+  return last <= c.extent;
+}
+
 bsa_status_t packed_attention(const bsa_tokens_t* t, bool shared, const void* q, const bsa_cache_t& k,
                               const bsa_cache_t& v, const float* o_own, const float* lse_own, void* o,
                               float* lse, float* o_f32, void* workspace, size_t workspace_bytes,
@@ -375,6 +387,9 @@ bsa_status_t packed_attention(const bsa_tokens_t* t, bool shared, const void* q,
   a.partial = shared ? 1 : 0;
   a.max_entries = w.max_entries;
   a.num_sms = num_sms;
+  while ((1 << a.lgG) < a.G) ++a.lgG;
+  a.k_safe = inside_extent(k, t);
+  a.v_safe = inside_extent(v, t);
   a.scale_log2 = (t->attn_scale > 0.f ? t->attn_scale : 1.0f / std::sqrt(static_cast<float>(t->d))) *
                  1.4426950408889634f;
   const cudaError_t e = bsa::launch_packed(a, tq, tk, tv, num_sms, static_cast<cudaStream_t>(stream));

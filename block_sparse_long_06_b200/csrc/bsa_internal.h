@@ -177,7 +177,8 @@ struct PackedArgs {
   float* part_ml;             // [smax, N, Hq, 2] (max, sum) in log2 units
   float* part_o;              // [smax, N, Hq, d] fp32, not normalised
   int N, B, Hq, Hkv, G, d, T, causal, smax, partial;   // partial: every row goes through part_*
-  int max_entries, num_sms;
+  int max_entries, num_sms, lgG;   // lgG: log2(G)
+  int k_safe, v_safe;         // every page (or block) of the cache lies inside its extent
   float scale_log2;
 };
 // Launch with programmatic stream serialization: the kernel's CTAs may start while

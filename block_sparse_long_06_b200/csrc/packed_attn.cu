@@ -40,7 +40,7 @@ namespace bsa {
 namespace {
 
 constexpr int kThreads = 384;          // warps 0-3 / 4-7: softmax of tile 0 / 1; then one each:
-constexpr int kSoftmaxWarps = 8, kWarpLoad = 8, kWarpMma = 9, kWarpPatch = 10;
+constexpr int kSoftmaxWarps = 8, kWarpLoad = 8, kWarpMma = 9, kWarpPatch = 10, kWarpQ = 11;
 // of every kPolyOf pairs of a row's scores, kPoly take their exponentials by polynomial
 constexpr int kPolyOf = 8, kPoly = 1;
 constexpr uint32_t kTmemCols = 512;
@@ -92,12 +92,6 @@ BSA_DEVFN void set_abort(Bars* b, int32_t* status) {
   report(status, BSA_DEV_TIMEOUT);
 }
 
-BSA_DEVFN bool warp_wait(uint64_t* bar, uint32_t parity) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity);
-  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-}
-
 BSA_DEVFN bool warp_wait_sleep(uint64_t* bar, uint32_t parity) {
   bool ok = true;
   if ((threadIdx.x & 31) == 0) ok = mbar_wait_sleep(bar, parity);
@@ -140,6 +134,35 @@ BSA_DEVFN float2 exp2_poly(float2 x) {
   p = __ffma2_rn(p, f, make_float2(1.0f, 1.0f));
   return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(r.x) << 23)),
                      __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(r.y) << 23)));
+}
+
+// Every thread holds 64 bytes (w) of its own row; the four threads of a quad exchange them so
+// that one store instruction writes 64 contiguous bytes of each of 8 rows. (With 16 bytes of 32
+// rows an instruction, the stores of a unit kept shared memory waiting for 11,000 cycles.)
+// base + to[i] * size: where the 64 bytes of the quad's i-th row go, if fits[i].
+BSA_DEVFN void store_quad(char* base, const int64_t (&to)[4], int size, const bool (&fits)[4], uint32_t (&w)[16]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int x = 1; x <= 2; x <<= 1) {   // chunk bit x goes to lane bit x, row bit x to chunk bit x
+    const bool high = (lane & x) != 0;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      if (p & x) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t& lo = w[4 * p + i];
+        uint32_t& hi = w[4 * (p | x) + i];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? lo : hi, x);
+        lo = high ? got : lo;
+        hi = high ? hi : got;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (fits[i])
+      *reinterpret_cast<uint4*>(base + to[i] * size + (lane & 3) * 16) =
+          make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
 // Row (of width d) of the first token of block blk of (b, g), or -1 where it is bad.
@@ -366,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem[];   // the swizzle needs 1024-byte tiles
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kOffBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int half_tok = 128 / a.G;      // tokens of one tile
+  const int half_tok = 128 >> a.lgG;      // tokens of one tile
   if ((smem_u32(smem) & 1023u) != 0) {   // dynamic shared memory starts on a 1 KB boundary
     if (threadIdx.x == 0) report(a.status, BSA_DEV_TIMEOUT);
     return;
@@ -375,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars->info_full[x], 1);
-      mbar_init(&bars->info_empty[x], 2 + kSoftmaxWarps);   // with the issuer and the patch warp
+      mbar_init(&bars->info_empty[x], 3 + kSoftmaxWarps);   // with the issuer, patch and Q warps
       mbar_init(&bars->q_full[x], 1);
       mbar_init(&bars->q_empty[x], 1);
       mbar_init(&bars->s_full[x], 1);
@@ -413,17 +436,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kSoftmaxWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kWarpLoad) {
-      // ---------------------------------------------------------------- Q / K / V
-      uint32_t un = 0, kc = 0, qc[2] = {0, 0};
+      // ------------------------------------------------------------------ units, K, V
+      uint32_t un = 0, kc = 0;
       bool ok = true, taken = false;
+      int next = 0;
       int entries = 0;
       while (ok) {
         const int slot = un & 1;
         Unit U = {-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
         int u = blockIdx.x;            // the first unit; the others come from the counter
         if (taken) {
-          if (lane == 0) u = static_cast<int>(gridDim.x) + atomicAdd(&a.head[1], 1);
-          u = __shfl_sync(0xffffffffu, u, 0);
+          u = static_cast<int>(gridDim.x) + __shfl_sync(0xffffffffu, next, 0);
         }
         // The heads of an entry are neighbours: the longest units of all heads start first
         // (prompts of 2K and 4K: 53 and 146 us, 69 and 168 with one head after the other), and
@@ -457,31 +480,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           return __any_sync(0xffffffffu, bad);
         };
+        // whether a block blk, blk + 32, .. of the unit is bad. Where every page of the cache lies
+        // inside its extent (safe), that is the page's number alone, and the loads of a lane do
+        // not wait for each other.
+        auto scan = [&](const CacheView& c, int safe, const Unit& U, int blk, int end) {
+          bool bad = false;
+          if (!safe) {
+            for (; blk < end; blk += 32) bad |= block_row(c, U.b, U.g, blk, U.len, D) < 0;
+          } else if (c.page_table != nullptr) {
+            const int32_t* pt = c.page_table + static_cast<int64_t>(U.b) * c.pt_stride;
+            const unsigned pages = c.num_pages;
+#pragma unroll 8
+            for (; blk < end; blk += 32) bad |= static_cast<unsigned>(pt[blk]) >= pages;
+          }
+          return bad;
+        };
         if (u < units) {
           U = {u, e0.x, g, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w & 0xffff, e1.w >> 16, 0};
           nblk = (U.len + kBlock - 1) / kBlock;
-          if (U.step1 > U.step0) {
-            const int ntiles = U.ntok > half_tok ? 2 : 1;
-            if (lane == 0) {
-              for (int t = 0; t < ntiles && ok; ++t) {
-                if (!mbar_wait_sleep(&bars->q_empty[t], (qc[t] & 1) ^ 1)) { ok = false; break; }
-                mbar_arrive_expect_tx(&bars->q_full[t], C::kTile);
-                for (int x = 0; x < C::kHalves; ++x)
-                  tma_load_3d(smem + t * C::kTile + x * C::kSlab, &tmq, x * 64, U.g * a.G,
-                              U.row0 + t * half_tok, &bars->q_full[t]);
-                ++qc[t];
-              }
-            }
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-            if (!ok) break;
-          }
           // blocks with a bad page or beyond the cache are found before the unit starts
           bool bad = look_up(2 * U.step0);
-          for (int first = 2 * U.step0 + 32; first < min(2 * U.step1, nblk) && !bad; first += 32) {
-            const int keep_k = rk, keep_v = rv;
-            bad = look_up(first);
-            rk = keep_k;
-            rv = keep_v;
+          const int end = min(2 * U.step1, nblk), from = 2 * U.step0 + 32;
+          if (from < end) {
+            bool later = scan(a.k, a.k_safe, U, from + lane, end);
+            if (a.v.page_table != a.k.page_table || !a.k_safe || !a.v_safe || a.v.num_pages < a.k.num_pages)
+              later |= scan(a.v, a.v_safe, U, from + lane, end);
+            bad |= __any_sync(0xffffffffu, later) != 0;
           }
           U.bad = bad ? 1 : 0;
           if (bad && lane == 0) report(a.status, BSA_DEV_BAD_PAGE);
@@ -497,6 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         if (!ok || U.u < 0 || aborted(bars)) break;
         ++un;
+        if (U.step1 <= U.step0 && lane == 0) next = atomicAdd(&a.head[1], 1);
         for (int s0 = U.step0; s0 < U.step1 && ok; s0 += 16) {
           if (s0 > U.step0) look_up(2 * s0);
           const int n_here = min(16, U.step1 - s0);
@@ -504,6 +529,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int k0 = __shfl_sync(0xffffffffu, rk, 2 * q), k1 = __shfl_sync(0xffffffffu, rk, 2 * q + 1);
             const int v0 = __shfl_sync(0xffffffffu, rv, 2 * q), v1 = __shfl_sync(0xffffffffu, rv, 2 * q + 1);
             if (lane == 0) {
+              // the next unit, shortly before this one's copies end: not earlier, since a unit
+              // waits while its block is busy
+              if (s0 + q == max(U.step1 - 3, U.step0)) next = atomicAdd(&a.head[1], 1);
               // a step that has the sequence's end or a bad block goes through the patch warp
               const bool patch = (s0 + q + 1) * kStep > U.len || k0 < 0 || k1 < 0;
               for (int kv = 0; kv < 2 && ok; ++kv, ++kc) {
@@ -530,8 +558,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         // copies in flight must land before the block exits (bounded)
         for (uint32_t k = (kc > NS ? kc - NS : 0); k < kc; ++k)
           mbar_wait_sleep(&bars->kv_full[k % NS], (k / NS) & 1, 100000000ull);
+      }
+    } else if (warp == kWarpQ && lane == 0) {
+      // ------------------------------------------------------------------------------ Q
+      // A warp of its own: Q of the next unit waits for the last scores of this one, and the
+      // copies of its keys must not wait with it (bubbles of 14,000 cycles between units).
+      uint32_t un = 0, phase = 0;      // phase: a bit for each tile
+      bool ok = true;
+      while (true) {
+        const int slot = un & 1;
+        ok = mbar_wait_sleep(&bars->info_full[slot], (un >> 1) & 1);
+        if (!ok) break;
+        const Unit U = bars->info[slot];
+        mbar_arrive(&bars->info_empty[slot]);
+        ++un;
+        if (U.u < 0 || aborted(bars)) break;
+        const int ntiles = U.step1 <= U.step0 ? 0 : U.ntok > half_tok ? 2 : 1;
+        for (int t = 0; t < ntiles && ok; ++t) {
+          ok = mbar_wait_sleep(&bars->q_empty[t], ((phase >> t) & 1) ^ 1);
+          if (!ok) break;
+          phase ^= 1u << t;
+          mbar_arrive_expect_tx(&bars->q_full[t], C::kTile);
+          for (int x = 0; x < C::kHalves; ++x)
+            tma_load_3d(smem + t * C::kTile + x * C::kSlab, &tmq, x * 64, U.g * a.G,
+                        U.row0 + t * half_tok, &bars->q_full[t]);
+        }
+        if (!ok) break;
+      }
+      if (!ok) {
+        set_abort(bars, a.status);
+        // copies in flight must land before the block exits (bounded): a tile's last copy has
+        // landed when q_full has left the phase before this one's
         for (int t = 0; t < 2; ++t)
-          if (qc[t] > 0) mbar_wait_sleep(&bars->q_full[t], (qc[t] - 1) & 1, 100000000ull);
+          mbar_wait_sleep(&bars->q_full[t], ((phase >> t) & 1) ^ 1, 100000000ull);
       }
     } else if (warp == kWarpPatch) {
       // -------------------------- V rows behind the end (or of a bad block) become zero
@@ -753,11 +812,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int stride = U.ntok <= half_tok ? 2 : 1;
       int left = U.step1 - U.step0 - (stride - 1) * t;
       {
-        const int tok0 = stride == 2 ? 0 : t * half_tok, tok = tok0 + row / a.G;
+        const int tok0 = stride == 2 ? 0 : t * half_tok, tok = tok0 + (row >> a.lgG);
         // the last key this row sees
         const int last = tok >= U.ntok ? -1 : a.causal ? min(U.pos0 + tok, U.len - 1) : U.len - 1;
         lim = last - (U.step0 + (stride - 1) * t) * kStep;
-        idle = tok0 + (quarter * 32) / a.G >= U.ntok;
+        idle = tok0 + ((quarter * 32) >> a.lgG) >= U.ntok;
       }
       for (; left > 0; left -= stride, lim -= stride * kStep, bits ^= 8) {
         if (!warp_wait_all(&bars->s_full[t], (bits >> 3) & 1)) { ok = false; break; }
