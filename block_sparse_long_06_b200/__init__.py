@@ -215,11 +215,22 @@ class Cache:
     page_table: Optional[torch.Tensor] = None
     num_pages: int = 0
 
+    def __setattr__(self, name, value):
+        # the struct is kept between calls until a field changes
+        object.__setattr__(self, name, value)
+        if name != "_kept":
+            object.__setattr__(self, "_kept", None)
+
     def c(self) -> CCache:
-        pt = self.page_table
-        return CCache(self.tensor.data_ptr(), self.seq_stride, self.block_stride, self.head_stride,
-                      None if pt is None else pt.data_ptr(),
-                      0 if pt is None else pt.shape[1], self.num_pages, self.tensor.numel())
+        pt, c = self.page_table, self._kept
+        if c is None:
+            c = self._kept = CCache(None, self.seq_stride, self.block_stride, self.head_stride,
+                                    None, 0 if pt is None else pt.shape[1], self.num_pages,
+                                    self.tensor.numel())
+        c.base = self.tensor.data_ptr()
+        if pt is not None:
+            c.page_table = pt.data_ptr()
+        return c
 
 
 def contiguous_cache(t: torch.Tensor) -> Cache:
@@ -373,17 +384,23 @@ class Tokens:
         return (self.cu_seqlens, self.seq_lens, self.positions, self.q_weight, self.k_weight,
                 None if rope is None else rope.steps)
 
-    def c(self) -> CTokens:
-        kept, tensors = self._kept, self.tensors()
-        # a rope object may have been changed in place: its fields are part of the key
-        key = None if self.rope is None else (self.rope.steps, self.rope.interleaved, self.rope.factor)
-        if kept is None or (kept[1] is not key and (kept[1] is None or key is None or
-                                                    kept[1][0] is not key[0] or kept[1][1:] != key[1:])):
-            kept = self._kept = (self._describe(), key)
+    def _description(self):
+        """(struct, device index or -1): checked once, then only the addresses are renewed."""
+        kept, rope = self._kept, self.rope
+        if kept is None or (rope is not None and (kept[3] is not rope.steps or
+                                                  kept[4] != (rope.interleaved, rope.factor))):
+            names = ("cu_seqlens", "seq_lens", "positions", "q_weight", "k_weight", "rope_steps")
+            given = [(n, t) for n, t in zip(names, self.tensors()) if t is not None]
+            kept = self._kept = (self._describe(), given[0][1].get_device() if given else -1, given,
+                                 None if rope is None else rope.steps,
+                                 None if rope is None else (rope.interleaved, rope.factor))
         c = kept[0]
-        c.cu_seqlens, c.seq_lens, c.positions, c.q_weight, c.k_weight, c.rope_steps = [
-            None if t is None else t.data_ptr() for t in tensors]
-        return c
+        for name, t in kept[2]:
+            setattr(c, name, t.data_ptr())
+        return c, kept[1]
+
+    def c(self) -> CTokens:
+        return self._description()[0]
 
     def _describe(self) -> CTokens:
         _want("cu_seqlens", self.cu_seqlens, torch.int32, (self.B + 1,))
@@ -402,13 +419,6 @@ class Tokens:
                        1.0 if rope is None else float(rope.factor), int(self.norm),
                        float(self.eps), None, None, int(self.causal), float(self.attn_scale),
                        int(self.q_stride))
-
-    def device_index(self):
-        """The device of the description's tensors, -1 without any."""
-        for t in self.tensors():
-            if t is not None:
-                return t.get_device()
-        return -1
 
 
 _ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
@@ -449,6 +459,13 @@ def _check_device(dev, *tensors):
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise BsaError(f"a tensor on {t.device}, wanted on cuda:{dev} as the others")
+
+
+def _tokens_on(tok, dev) -> CTokens:
+    c, at = tok._description()
+    if at != dev and at != -1:
+        raise BsaError(f"the description's tensors are on cuda:{at}, the others on cuda:{dev}")
+    return c
 
 
 def _raw_stream(stream, dev) -> int:
@@ -552,10 +569,9 @@ def bsa_norm_rope(tok: Tokens, q, q_out, k=None, k_out=None, dev_status=None, st
     if (q is None) != (q_out is None) or (k is None) != (k_out is None) or q is k is None:
         raise BsaError("bsa_norm_rope: q and q_out, k and k_out come together, one pair at least")
     dev = (k if q is None else q).get_device()
-    N, d, c = tok.N, tok.d, tok.c()
-    if tok.device_index() not in (-1, dev):
-        raise BsaError("bsa_norm_rope: the description's tensors are on another device")
-    _check_device(dev, dev_status)
+    N, d, c = tok.N, tok.d, _tokens_on(tok, dev)
+    if dev_status is not None:
+        _check_device(dev, dev_status)
     _launch(load_library().bsa_norm_rope, "bsa_norm_rope", dev, c,
             _rows("q", q, N, tok.Hq, d, dev), _rows("q_out", q_out, N, tok.Hq, d, dev, True),
             _rows("k", k, N, tok.Hkv, d, dev), _rows("k_out", k_out, N, tok.Hkv, d, dev, True),
@@ -571,9 +587,7 @@ def bsa_append_kv(tok: Tokens, k, v, k_cache: Cache, v_cache: Cache, k_idx=None,
     if (q is None) != (q_out is None) or (k_idx is None) != (kidx_cache is None):
         raise BsaError("bsa_append_kv: q and q_out, k_idx and kidx_cache come together")
     dev = k.get_device()
-    N, d, H, c = tok.N, tok.d, tok.Hkv, tok.c()
-    if tok.device_index() not in (-1, dev):
-        raise BsaError("bsa_append_kv: the description's tensors are on another device")
+    N, d, H, c = tok.N, tok.d, tok.Hkv, _tokens_on(tok, dev)
     _check_device(dev, dev_status, k_cache.tensor, k_cache.page_table, v_cache.tensor,
                   v_cache.page_table)
     if kidx_cache is not None:
@@ -601,9 +615,7 @@ def _packed_call(name, tok, q, k, v, own, o, lse, o_f32, workspace, dev_status, 
             N > 0 and (stride[2] != 1 or stride[1] != d)):
         raise BsaError(f"{name}: q has to be bfloat16 [{N}, {Hq}, {d}] on the GPU, a token's "
                        f"heads side by side, got {q.dtype} {tuple(q.shape)} {q.stride()}")
-    c = tok.c()
-    if tok.device_index() not in (-1, dev):
-        raise BsaError(f"{name}: the description's tensors are on another device")
+    c = _tokens_on(tok, dev)
     _check_device(dev, k.tensor, k.page_table, v.tensor, v.page_table, o, lse, o_f32, workspace,
                   dev_status, *own)
     _want("o", o, torch.bfloat16, (N, Hq, d))
