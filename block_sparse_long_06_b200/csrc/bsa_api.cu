@@ -230,6 +230,15 @@ bsa_status_t check_rows(const bsa_rows_t& x, int type) {
   return BSA_OK;
 }
 
+// Output rows (bf16) of N tokens and `heads` heads: heads may not overlap.
+bsa_status_t check_out(const bsa_rows_t& x, const bsa_tokens_t* t, int heads) {
+  bsa_status_t st = check_rows(x, BSA_TYPE_BF16);
+  if (st != BSA_OK) return st;
+  if ((t->N > 1 && x.token_stride < t->d) || (heads > 1 && x.head_stride < t->d))
+    return BSA_ERR_INVALID_ARG;
+  return BSA_OK;
+}
+
 // An output that starts where its input does has to be the same rows.
 bool same_or_apart(const bsa_rows_t& in, const bsa_rows_t& out) {
   return in.base != out.base || (in.type == out.type && in.token_stride == out.token_stride &&
@@ -800,14 +809,14 @@ bsa_status_t bsa_norm_rope(const bsa_tokens_t* t, bsa_rows_t q, bsa_rows_t q_out
     return BSA_ERR_INVALID_ARG;
   bsa::HeadsArgs a = heads_args(t, type, dev_status);
   if (q.base != nullptr) {
-    if ((st = check_rows(q, type)) != BSA_OK || (st = check_rows(q_out, BSA_TYPE_BF16)) != BSA_OK)
+    if ((st = check_rows(q, type)) != BSA_OK || (st = check_out(q_out, t, t->Hq)) != BSA_OK)
       return st;
     if (!same_or_apart(q, q_out)) return BSA_ERR_INVALID_ARG;
     a.q = rows_view(q);
     a.q_out = rows_view(q_out);
   }
   if (k.base != nullptr) {
-    if ((st = check_rows(k, type)) != BSA_OK || (st = check_rows(k_out, BSA_TYPE_BF16)) != BSA_OK)
+    if ((st = check_rows(k, type)) != BSA_OK || (st = check_out(k_out, t, t->Hkv)) != BSA_OK)
       return st;
     if (!same_or_apart(k, k_out)) return BSA_ERR_INVALID_ARG;
     a.k = rows_view(k);
@@ -844,7 +853,7 @@ bsa_status_t bsa_append_kv(const bsa_tokens_t* t, bsa_rows_t k, bsa_rows_t v, bs
     a.kidx_cache = view(kidx_cache);
   }
   if (q.base != nullptr) {
-    if ((st = check_rows(q, type)) != BSA_OK || (st = check_rows(q_out, BSA_TYPE_BF16)) != BSA_OK)
+    if ((st = check_rows(q, type)) != BSA_OK || (st = check_out(q_out, t, t->Hq)) != BSA_OK)
       return st;
     if (!same_or_apart(q, q_out)) return BSA_ERR_INVALID_ARG;
     a.q = rows_view(q);

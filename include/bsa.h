@@ -286,14 +286,18 @@ bsa_status_t bsa_score_blocks_q(const bsa_problem_t* prob, const void* q_idx, bs
  * Token rows. N rows lie packed: sequence b has the rows [cu_seqlens[b],
  * cu_seqlens[b+1]), in order, and its last row is its newest token, so that row i of
  * sequence b is token seq_lens[b] - (cu_seqlens[b+1] - i) of it. Rows behind
- * cu_seqlens[B] are padding: nothing of theirs is read or written. Lengths live on
- * the device, so a captured graph serves changing lengths.
+ * cu_seqlens[B] are padding: nothing of theirs is written, and what they hold has no
+ * effect. Lengths live on the device, so a captured graph serves changing lengths.
+ * Calls whose work may overlap need workspaces (and outputs) of their own. Results do
+ * not depend on the order in which the GPU does the work: the same call gives the
+ * same bits.
  * ---------------------------------------------------------------------- */
 typedef enum { BSA_TYPE_BF16 = 0, BSA_TYPE_F16 = 1, BSA_TYPE_F32 = 2 } bsa_type_t;
 
 /* Head rows in memory: element c of head h of row n is element
  * n*token_stride + h*head_stride + c from `base`; the elements of one head are
- * contiguous and start on a 16-byte boundary (base and strides). base = NULL: none. */
+ * contiguous and start on a 16-byte boundary (base and strides). A stride of 0 reads
+ * one row for all; the heads of an output may not overlap. base = NULL: none. */
 typedef struct {
   void* base;
   int64_t token_stride;      /* elements */
@@ -344,7 +348,7 @@ bsa_status_t bsa_norm_rope(const bsa_tokens_t* tok, bsa_rows_t q, bsa_rows_t q_o
  * token's slot of k_cache, v_cache and kidx_cache. Where q.base is not NULL its heads
  * are normed and rotated into q_out by the same launch. A row whose slot does not
  * exist (bad page, outside the extent) is not written and reported. Two rows with
- * the same slot (a page that two sequences share) leave either's values. */
+ * the same slot (a page that two sequences share) leave a mixture of both. */
 bsa_status_t bsa_append_kv(const bsa_tokens_t* tok, bsa_rows_t k, bsa_rows_t v, bsa_rows_t kidx,
                            bsa_cache_t k_cache, bsa_cache_t v_cache, bsa_cache_t kidx_cache,
                            bsa_rows_t q, bsa_rows_t q_out, int32_t* dev_status, void* stream);

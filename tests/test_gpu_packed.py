@@ -172,6 +172,51 @@ def test_single_tokens_split_over_keys(lens):
     assert torch.equal(again.o, step.o) and torch.equal(again.lse, step.lse)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_row_over_many_splits(d):
+    """More splits than a warp has lanes are joined; three kv heads."""
+    n, G, Hkv = 40000, 4, 3
+    mem = Paged([n], Hkv, d, seed=23)
+    q = randn(1, Hkv * G, d, seed=24, scale=2.0)
+    step = run_attend(q, mem, [0, 1], [n], Hkv)
+    check(step, exact(q, mem, [0, 1], [n], True, G), n, d)
+
+
+def test_the_same_call_gives_the_same_bits():
+    d, G, Hkv = 128, 4, 2
+    lens, new = [1500, 700, 3000, 64], [200, 1, 3, 64]
+    cu = sums(new)
+    mem = Paged(lens, Hkv, d, seed=25)
+    q = randn(cu[-1], Hkv * G, d, seed=26)
+    first = run_attend(q, mem, cu, lens, Hkv)
+    for _ in range(5):
+        again = run_attend(q, mem, cu, lens, Hkv)
+        assert torch.equal(first.o_f32, again.o_f32) and torch.equal(first.lse, again.lse)
+
+
+def test_two_streams_at_once():
+    """Two objects, each with a workspace of its own, on two streams; inputs of one made on the
+    other's stream are waited for by the caller."""
+    d, G, Hkv = 128, 4, 2
+    lens, new = [900, 3000], [100, 1]
+    cu = sums(new)
+    mem = Paged(lens, Hkv, d, seed=27)
+    qs = [randn(cu[-1], Hkv * G, d, seed=28 + i) for i in range(2)]
+    steps, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for q in qs:
+        tok = bsa.Tokens(N=cu[-1], B=2, Hq=Hkv * G, Hkv=Hkv, d=d, T=mem.T, cu_seqlens=ints(cu),
+                         seq_lens=ints(lens))
+        steps.append(bsa.PackedAttention(tok))
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for q, step, stream in zip(qs, steps, streams):
+            step.run(q, *mem.caches(), stream=stream)
+    torch.cuda.synchronize()
+    for q, step in zip(qs, steps):
+        assert int(step.status.item()) == 0
+        check(step, exact(q, mem, cu, lens, True, G), 3000, d)
+
+
 def test_growing_scores_move_the_maximum():
     """Each block of keys has larger scores than the ones before, so O is rescaled many times;
     one key late in the row takes nearly all the weight."""

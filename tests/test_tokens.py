@@ -173,6 +173,8 @@ def test_bad_rows_are_refused(lib):
     assert call(t, rows(), rows(0x20000), rows(kind=1), rows(0x30000), None, None) == E  # two types
     assert call(t, rows(), rows(ts=2048), NONE, NONE, None, None) == E      # in place, other rows
     assert call(t, rows(kind=2), rows(), NONE, NONE, None, None) == E       # in place, other type
+    for bad in (rows(0x20000, ts=0), rows(0x20000, hs=0), rows(0x20000, hs=64)):   # heads overlap
+        assert call(t, rows(), bad, NONE, NONE, None, None) == E
     app = lib.bsa_append_kv
     assert app(t, rows(), rows(kind=1), NONE, cache(), cache(), bsa.CCache(), NONE, NONE, None,
                None) == E
