@@ -403,6 +403,37 @@ def test_shared_prefix(d, G, rows, lens, with_own):
     check(step, exact_shared(q, mem, cu, lens, G, own), max(lens), d)
 
 
+@pytest.mark.parametrize("d,G,Hkv", [(128, 4, 8), (64, 8, 3)])
+def test_work_dealt_to_the_sms_in_equal_parts(d, G, Hkv):
+    """Few tiles of very different lengths, a prefix without tokens and one of a single block
+    among them: tiles are cut wherever an SM's share ends."""
+    rows, lens = [30, 1, 64, 2, 17], [9000, 0, 2500, 64, 5001]
+    cu = sums(rows)
+    mem = Paged(lens, Hkv, d, seed=78)
+    q = randn(cu[-1], Hkv * G, d, seed=79, scale=1.5)
+    own = (torch.randn(cu[-1], Hkv * G, d, generator=gen(80), device="cuda"),
+           8.0 + torch.randn(cu[-1], Hkv * G, generator=gen(81), device="cuda"))
+    step = run_shared(q, mem, cu, lens, Hkv, own)
+    check(step, exact_shared(q, mem, cu, lens, G, own), max(lens), d)
+
+
+def test_shared_prefix_bad_ranges_write_nothing():
+    mem = Paged([100, 100], 1, 64, seed=82)
+    q = randn(10, 2, 64, seed=83)
+    good = bsa.Tokens(N=10, B=2, Hq=2, Hkv=1, d=64, T=mem.T, cu_seqlens=ints([0, 5, 10]),
+                      seq_lens=ints([100, 100]))
+    step = bsa.SharedPrefixDecode(good)
+    step.run(q, *mem.caches())                   # leaves results in the workspace
+    for cu in ([0, 6, 4], [0, 4, 11], [1, 4, 10]):
+        good.cu_seqlens = ints(cu)
+        step.status.zero_()
+        step.o.fill_(77.0)
+        step.lse.fill_(77.0)
+        step.run(q, *mem.caches())
+        assert int(step.status.item()) == bsa.BSA_DEV_BAD_LENGTH
+        assert (step.o == 77.0).all() and (step.lse == 77.0).all()
+
+
 def test_shared_prefix_outputs_may_be_the_own_part():
     d, G, Hkv = 128, 4, 2
     mem = Paged([300], Hkv, d, seed=74)
