@@ -297,7 +297,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) 
   // Without splits the SMs are evenly loaded where there are several units for each SM and the
   // costliest (started first) is no more than an SM's share. Else the cost that a unit may have
   // is searched, a warp for each candidate: the time is the costliest unit's where every unit
-  // has an SM of its own, and otherwise an SM's share of all costs and half of the costliest.
+  // has an SM of its own, and otherwise the units in whole rounds of the SMs, and no less than an
+  // SM's share of all costs and a third of the costliest (SMs are not equally fast).
   // A unit costs kUnitCost besides its steps, a merge kMergeCost and as much as a step for each
   // kRowsCost partial rows that are written and read again.
   const float share = static_cast<float>(work) * a.Hkv / a.num_sms;
@@ -319,8 +320,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) 
     const float unit = piece + kUnitCost;
     const float merge = (parts > 0 && !a.partial ? kMergeCost : 0.f) +
                         static_cast<float>(parts) * a.Hkv / (kRowsCost * a.num_sms);
-    const float time =
-        merge + (units <= a.num_sms ? unit : share + units * kUnitCost / a.num_sms + 0.5f * unit);
+    // an SM's share of all costs; its share of the units in whole rounds
+    const float even = share + units * kUnitCost / a.num_sms;
+    const float rounds = even * a.num_sms / max(units, 1) * ((units + a.num_sms - 1) / a.num_sms);
+    const float time = merge + (units <= a.num_sms ? unit : max(rounds, even + 0.35f * unit));
     if (lane == 0) atomicMin(&best, (static_cast<unsigned long long>(__float_as_uint(time)) << 32) |
                                         static_cast<unsigned>(cand));
     __syncthreads();
