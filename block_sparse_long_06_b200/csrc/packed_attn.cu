@@ -136,35 +136,6 @@ BSA_DEVFN float2 exp2_poly(float2 x) {
                      __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(r.y) << 23)));
 }
 
-// Every thread holds 64 bytes (w) of its own row; the four threads of a quad exchange them so
-// that one store instruction writes 64 contiguous bytes of each of 8 rows. (With 16 bytes of 32
-// rows an instruction, the stores of a unit kept shared memory waiting for 11,000 cycles.)
-// base + to[i] * size: where the 64 bytes of the quad's i-th row go, if fits[i].
-BSA_DEVFN void store_quad(char* base, const int64_t (&to)[4], int size, const bool (&fits)[4], uint32_t (&w)[16]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int x = 1; x <= 2; x <<= 1) {   // chunk bit x goes to lane bit x, row bit x to chunk bit x
-    const bool high = (lane & x) != 0;
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      if (p & x) continue;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t& lo = w[4 * p + i];
-        uint32_t& hi = w[4 * (p | x) + i];
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? lo : hi, x);
-        lo = high ? got : lo;
-        hi = high ? hi : got;
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (fits[i])
-      *reinterpret_cast<uint4*>(base + to[i] * size + (lane & 3) * 16) =
-          make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-}
-
 // Row (of width d) of the first token of block blk of (b, g), or -1 where it is bad.
 BSA_DEVFN int64_t block_row(const CacheView& c, int b, int g, int blk, int len, int d) {
   int64_t phys = blk;
