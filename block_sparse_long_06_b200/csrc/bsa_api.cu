@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "bsa_internal.h"
+#include "tokens_internal.h"
 
 namespace {
 

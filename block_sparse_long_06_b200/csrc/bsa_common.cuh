@@ -128,16 +128,6 @@ BSA_DEVFN void tma_load_2d(void* dst, const CUtensorMap* map, int32_t x, int32_t
       : "memory");
 }
 
-// As tma_load_2d for a 3-D map; y and z have no alignment rule.
-BSA_DEVFN void tma_load_3d(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
-                           uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
-      "{%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
-}
-
 BSA_DEVFN void prefetch_tensormap(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
@@ -207,10 +197,6 @@ BSA_DEVFN float2 unpack_bf16(uint32_t x) {
 // launched with launch_pdl call it before touching any buffer an earlier kernel of
 // the stream reads or writes; the code before it only sets up shared memory.
 BSA_DEVFN void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-// Let the kernel launched behind this one (launch_pdl) start its own setup already; its
-// grid_dependency_wait still waits for this whole grid.
-BSA_DEVFN void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Value of an E4M3 (FP8, bias 7, with subnormals) code; 0x7F (NaN) is never produced
 // by the index-key quantiser.

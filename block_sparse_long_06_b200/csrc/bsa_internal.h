@@ -135,52 +135,6 @@ struct PbsArgs {
   float scale_log2;
 };
 
-// Device-side copy of a bsa_rows_t.
-struct RowsView {
-  void* base;
-  int64_t token_stride, head_stride;
-};
-
-// Head norms and rotary positions of new token rows, into tensors or the caches.
-struct HeadsArgs {
-  RowsView q, k, v, kidx;     // inputs of one type (bsa_type_t); base null: none
-  RowsView q_out, k_out;      // bf16; k_out unused when `cached`
-  CacheView k_cache, v_cache, kidx_cache;   // when `cached`: where k, v and kidx go
-  const int32_t* cu;          // [B+1] or null
-  const int32_t* seq_lens;    // [B] or null
-  const int32_t* positions;   // [N] or null
-  const uint64_t* rope_steps; // [rope_dim / 2]
-  const float* q_weight;      // [d] or null
-  const float* k_weight;      // [d] or null
-  int32_t* status;
-  int N, B, Hq, Hkv, d, T, type, cached, needs_slot;   // needs_slot: rows look up their sequence
-  int rope_dim, rope_interleaved, norm;
-  float rope_factor, eps;
-};
-
-// Dense attention of packed rows (workspace pointers: the plan kernel's results, partials).
-struct PackedArgs {
-  const void* q;
-  CacheView k, v;
-  const int32_t* cu;          // [B+1] or null
-  const int32_t* seq_lens;    // [B] or null
-  const float* o_own;         // [N, Hq, d] or null: joined by the merge
-  const float* lse_own;       // [N, Hq]
-  void* o;                    // [N, Hq, d] bf16
-  float* lse;                 // [N, Hq]
-  float* o_f32;               // [N, Hq, d] or null
-  int32_t* status;
-  int32_t* head;              // plan: [0] entries, [1] unit counter, [2] any row split
-  int32_t* offs;              // plan: [B+1] first tile of each sequence
-  int4* entries;              // plan: two int4 an entry
-  int32_t* row_splits;        // plan: [N] partial results of each row (0: row not written)
-  float* part_ml;             // [smax, N, Hq, 2] (max, sum) in log2 units
-  float* part_o;              // [smax, N, Hq, d] fp32, not normalised
-  int N, B, Hq, Hkv, G, d, T, causal, smax, partial;   // partial: every row goes through part_*
-  int max_entries, num_sms, lgG;   // lgG: log2(G)
-  int k_safe, v_safe;         // every page (or block) of the cache lies inside its extent
-  float scale_log2;
-};
 // Launch with programmatic stream serialization: the kernel's CTAs may start while
 // the previous kernel of the stream drains; the kernel orders itself after it with
 // grid_dependency_wait(). Hides launch latency between the steps of the path.
@@ -221,12 +175,6 @@ cudaError_t launch_prefill_tc(const PrefillArgs& a, const CUtensorMap& tq, const
 cudaError_t launch_pbs_permute(const PbsArgs& a, int num_sms, cudaStream_t s);
 // Key chunks (CTAs per (b, g)) of the importance passes.
 int pbs_chunks(int T);
-
-cudaError_t launch_token_heads(const HeadsArgs& a, int num_sms, cudaStream_t s);
-cudaError_t launch_packed(const PackedArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
-                          const CUtensorMap& tv, int num_sms, cudaStream_t s);
-// Query rows (tokens) of one unit of the packed attention: two tiles of 128 (token, head) rows.
-constexpr int packed_unit_tokens(int G) { return 256 / G; }
 
 // Blocks per work item of the decode scorer (items are (row, chunk) pairs).
 int score_decode_chunk_blocks();

@@ -32,9 +32,9 @@
 //    step is handed to the tensor cores. K there may be anything: its scores are replaced.
 // Tensor memory: O of tile t at 128 t, S (and P) of tile t at 256 + 128 t. Every wait is
 // bounded; on a timeout the kernel reports BSA_DEV_TIMEOUT, drains and returns.
-#include "bsa_common.cuh"
-#include "bsa_internal.h"
 #include "tcgen05.cuh"
+#include "tokens_common.cuh"
+#include "tokens_internal.h"
 
 namespace bsa {
 namespace {
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         kc += 2 * max(0, n);
       }
-    } else if (warp == kWarpMma && tc::elect()) {
+    } else if (warp == kWarpMma && elect_one()) {
       // ------------------------------------------------- MMA issuer of both tiles
       // One thread, the tiles in turn: P V (j) and S (j + 1) of tile 0, then of tile 1. The
       // tensor cores work in that order, so the tiles' softmax phases are half a period

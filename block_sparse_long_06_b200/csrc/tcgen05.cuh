@@ -84,16 +84,6 @@ BSA_DEVFN void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_
       : "memory");
 }
 
-// One lane of a converged warp, the same one every time. MMAs issued under `if (elect())` by a
-// warp whose operands are warp-uniform take about 45 cycles each to issue; under `if (lane == 0)`
-// about 85 (measured, batches of 8).
-BSA_DEVFN bool elect() {
-  uint32_t r;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
-               : "=r"(r));
-  return r != 0;
-}
-
 // ---------------------------------------------------------------- TMEM <-> registers
 // Each thread of the warp reads its lane (row) of 32 consecutive 32-bit columns.
 BSA_DEVFN void ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -107,16 +97,6 @@ BSA_DEVFN void ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
         "=r"(r[31])
-      : "r"(taddr));
-}
-// Each thread of the warp reads its lane of 16 consecutive 32-bit columns.
-BSA_DEVFN void ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
 // Each thread writes its lane of 16 consecutive 32-bit columns.
@@ -181,18 +161,6 @@ BSA_DEVFN void st16x128_x16(uint32_t taddr, const uint32_t (&r)[32]) {
 }
 
 BSA_DEVFN void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-// As wait_ld, and nothing that reads r can be moved in front of it: for a load issued well
-// before its wait.
-BSA_DEVFN void wait_ld_into(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
-                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]),
-                 "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]),
-                 "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
-}
 BSA_DEVFN void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 }  // namespace tc

@@ -17,8 +17,8 @@
 // warps share a row's heads.
 #include <type_traits>
 
-#include "bsa_common.cuh"
-#include "bsa_internal.h"
+#include "tokens_common.cuh"
+#include "tokens_internal.h"
 
 namespace bsa {
 namespace {

@@ -1,0 +1,31 @@
+// Device helpers of the operators on new token rows.
+#pragma once
+
+#include "bsa_common.cuh"
+
+namespace bsa {
+
+// As tma_load_2d for a 3-D map; y and z have no alignment rule.
+BSA_DEVFN void tma_load_3d(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                           uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Let the kernel launched behind this one (launch_pdl) start its own setup already; its
+// grid_dependency_wait still waits for this whole grid.
+BSA_DEVFN void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// One lane of a converged warp, the same one every time. MMAs issued under `if (elect_one())`
+// take about 45 cycles each to issue, under `if (lane == 0)` about 85 (measured, batches of 8).
+BSA_DEVFN bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(r));
+  return r != 0;
+}
+
+}  // namespace bsa
