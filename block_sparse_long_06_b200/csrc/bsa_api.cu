@@ -292,7 +292,7 @@ struct PackedWorkspace {
   int smax, max_entries;
   size_t offs, entries, row_splits, ml, o, total;
 };
-PackedWorkspace packed_workspace(const bsa_tokens_t* t, bool shared, int num_sms) {
+PackedWorkspace packed_workspace(const bsa_tokens_t* t, int num_sms) {
   PackedWorkspace w;
   const int per = bsa::packed_unit_tokens(t->Hq / t->Hkv);
   const int64_t rows = t->N > 0 ? t->N : 1;
@@ -300,13 +300,16 @@ PackedWorkspace packed_workspace(const bsa_tokens_t* t, bool shared, int num_sms
   const int64_t want = (4ll * num_sms + least * t->Hkv - 1) / (least * t->Hkv);
   const int64_t steps = (t->T + 127) / 128;
   w.smax = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, 64), steps)));
-  if (steps <= 2) w.smax = 1;   // a split has the cost of 4 steps of one tile at least
+  // A merge costs as much as 6 steps of one tile: halving 12 of them gains nothing, and without
+  // splits no merge is launched (4 rows behind 1,024 keys: 16 us, 20 with a merge that finds
+  // nothing to do).
+  if (steps * (t->N > per / 2 ? 2 : 1) <= 12) w.smax = 1;
   w.max_entries = static_cast<int>((least + std::min<int64_t>(rows, t->B)) * w.smax);
   w.offs = 256;
   w.entries = w.offs + align256((static_cast<size_t>(t->B) + 1) * sizeof(int32_t));
   w.row_splits = w.entries + align256(static_cast<size_t>(w.max_entries) * 2 * sizeof(int4));
   w.ml = w.row_splits + align256(static_cast<size_t>(rows) * sizeof(int32_t));
-  const size_t parts = w.smax > 1 || shared ? static_cast<size_t>(w.smax) * rows * t->Hq : 0;
+  const size_t parts = w.smax > 1 ? static_cast<size_t>(w.smax) * rows * t->Hq : 0;
   w.o = w.ml + align256(parts * 2 * sizeof(float));
   w.total = w.o + align256(parts * t->d * sizeof(float));
   return w;
@@ -359,7 +362,7 @@ bsa_status_t packed_attention(const bsa_tokens_t* t, bool shared, const void* q,
   if ((st = check_token_cache(k, t, t->d, true)) != BSA_OK) return st;
   if ((st = check_token_cache(v, t, t->d, true)) != BSA_OK) return st;
   const int num_sms = num_sms_current();
-  const PackedWorkspace w = packed_workspace(t, shared, num_sms);
+  const PackedWorkspace w = packed_workspace(t, num_sms);
   if (workspace == nullptr || workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255))
     return BSA_ERR_WORKSPACE;
   CUtensorMap tq, tk, tv;
@@ -394,9 +397,11 @@ bsa_status_t packed_attention(const bsa_tokens_t* t, bool shared, const void* q,
   a.T = t->T;
   a.causal = shared ? 0 : t->causal;
   a.smax = w.smax;
-  a.partial = shared ? 1 : 0;
   a.max_entries = w.max_entries;
   a.num_sms = num_sms;
+  const int max_tiles = w.max_entries / w.smax;
+  // (plan_in_warp has the reason and what it measured)
+  a.in_block = t->B <= 32 && max_tiles <= 32 && max_tiles * t->Hkv <= num_sms;
   while ((1 << a.lgG) < a.G) ++a.lgG;
   a.k_safe = inside_extent(k, t);
   a.v_safe = inside_extent(v, t);
@@ -874,7 +879,7 @@ bsa_status_t bsa_packed_workspace_size(const bsa_tokens_t* t, int32_t op, size_t
   if (st != BSA_OK) return st;
   if (op != BSA_OP_ATTEND_PACKED && op != BSA_OP_DECODE_SHARED) return BSA_ERR_INVALID_ARG;
   if (!is_pow2_group(t->Hq / t->Hkv)) return BSA_ERR_UNSUPPORTED;
-  *bytes = packed_workspace(t, op == BSA_OP_DECODE_SHARED, num_sms_current()).total;
+  *bytes = packed_workspace(t, num_sms_current()).total;
   return BSA_OK;
 }
 

@@ -15,8 +15,8 @@
 //    results are joined when they are written.
 //  * A step is 128 keys (two blocks of the cache). The loader warp copies K and V of a step
 //    into a ring of 32 KB stages; one issuing thread runs S = Q K^T into the tile's 128
-//    columns of tensor memory and O += P V from it; 8 softmax warps per tile (two threads a
-//    row, 64 keys each) turn S into P, written as bf16 over S. The two tiles take turns:
+//    columns of tensor memory and O += P V from it; four softmax warps per tile, a thread a
+//    row, turn S into P, written as bf16 over S. The two tiles take turns:
 //    while one is in its softmax, the other has the tensor cores. P V (j) and S (j + 1) of a
 //    tile are issued by the same thread, in order, so S needs no second buffer and the
 //    arrival of S (j + 1) says that P V (j) is done.
@@ -24,9 +24,12 @@
 //    in tensor memory. P <= 2^8 is rounded to bf16 (at most 2^-8 of each term, as much as the
 //    output's own rounding, and averaged over a row's terms); l sums the fp32 values. V stays
 //    bf16, so no value range is lost.
-//  * Few rows over many keys: the plan kernel (one block) cuts units into splits of the key
-//    axis, until the SMs are filled; each writes its O, m and l in fp32 and the merge kernel
-//    joins them. Units are handed out longest first.
+//  * Four more warps write a unit's result from tensor memory while the softmax warps are in
+//    the next unit's first steps (with the softmax warps writing it, 10,000 cycles a unit).
+//  * Few rows over many keys: a plan (a kernel of one block or, for few tiles, each block for
+//    itself) cuts units into splits of the key axis, until the SMs are filled; each writes its
+//    O, m and l in fp32 and the merge kernel joins them. Units are handed out longest first.
+//    What a row's own tokens gave is joined by whoever writes the row.
 //  * Rows of V behind a sequence's end are whatever the page held before: a patch warp
 //    zeroes them in shared memory in the step that has the end (0 * NaN is NaN), before the
 //    step is handed to the tensor cores. K there may be anything: its scores are replaced.
@@ -39,10 +42,14 @@
 namespace bsa {
 namespace {
 
-constexpr int kThreads = 384;          // warps 0-3 / 4-7: softmax of tile 0 / 1; then one each:
+constexpr int kThreads = 512;          // warps 0-3 / 4-7: softmax of tile 0 / 1; then one each:
 constexpr int kSoftmaxWarps = 8, kWarpLoad = 8, kWarpMma = 9, kWarpPatch = 10, kWarpQ = 11;
+constexpr int kWarpOut = 12;           // and 12-15: results
 // of every kPolyOf pairs of a row's scores, kPoly take their exponentials by polynomial
 constexpr int kPolyOf = 8, kPoly = 1;
+// registers a thread of the softmax warps, of the warps 8-11 and of 12-15
+constexpr int kRegsSoftmax = 192, kRegsOther = 64, kRegsOut = 64;
+static_assert(2 * kRegsSoftmax + kRegsOther + kRegsOut <= 65536 / 128, "registers of the launch");
 constexpr uint32_t kTmemCols = 512;
 constexpr int kStep = 128;             // keys a step
 constexpr int kMaxStages = 10;
@@ -72,10 +79,11 @@ struct Bars {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], kv_raw[kMaxStages];
   uint64_t s_full[2], o_full[2];
   uint64_t p_ready[2][2];              // [tile][half of the step's keys]
-  uint64_t pair[4];                    // [quarter of the rows]: its warps of both tiles
+  uint64_t ml_full[2], o_empty[2];     // a unit's (m, l) is written; its O and (m, l) are read
   uint64_t mma_done;
-  float2 swap[2][128];                 // [tile][row]: (m, l) of the tile
+  float2 ml[2][128];                   // [tile][row]
   Unit info[2];
+  int4 own[4];                         // the block's two entries, where it plans for itself
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -117,11 +125,11 @@ BSA_DEVFN float max3(float x, float y, float z) {
 // 2^x on the FMA pipes, two lanes at once, for x <= 8: x = n + f with n the nearest integer
 // (adding 1.5 * 2^23 rounds it into the low mantissa bits), 2^f by a quartic of least relative
 // error on [-1/2, 1/2] among those that are exactly 1 at 0 (Remez exchange, exp2_poly_fit.py:
-// 3.6e-6, so the fp32 sum l keeps 18 bits; the bf16 P needs 9), n added to the exponent field.
+// 2.8e-6, so the fp32 sum l keeps 18 bits; the bf16 P needs 9), n added to the exponent field.
 // x is clamped at -127, where that gives exactly 0: masked scores add nothing.
 BSA_DEVFN float2 exp2_poly(float2 x) {
-  constexpr float kC1 = 0.6931136250495911f, kC2 = 0.24020710587501526f;
-  constexpr float kC3 = 0.055976882576942444f, kC4 = 0.009782912209630013f;
+  constexpr float kC1 = 0.6931241750717163f, kC2 = 0.24024099111557007f;
+  constexpr float kC3 = 0.055906426161527634f, kC4 = 0.009582852944731712f;
   constexpr float kShift = 12582912.0f;  // 1.5 * 2^23
   x.x = fmaxf(x.x, -127.0f);
   x.y = fmaxf(x.y, -127.0f);
@@ -160,6 +168,34 @@ BSA_DEVFN int seq_first(const PackedArgs& a, int b) {
 }
 BSA_DEVFN int seq_len(const PackedArgs& a, int b) {
   return a.seq_lens != nullptr ? max(0, min(a.seq_lens[b], a.T)) : a.T;
+}
+
+// Without splits the SMs are evenly loaded where there are several units for each SM and the
+// costliest (started first) is no more than an SM's share. Else the cost that a unit may have is
+// searched among 32 candidates. The time with one is the costliest unit's where every unit has an
+// SM of its own, and otherwise the units in whole rounds of the SMs, and no less than an SM's
+// share of all costs and a third of the costliest (SMs are not equally fast). A unit costs
+// kUnitCost besides its steps, a merge kMergeCost and as much as a step for each kRowsCost
+// partial rows that are written and read again.
+BSA_DEVFN int candidate(int i, float share) {
+  return i == 0 ? 1 << 30 : max(4, static_cast<int>(share * (0.1f + 0.06f * i)) + 1);
+}
+// What a tile of cost c and ntok tokens adds under the candidate: units and the rows (of one kv
+// head) that go through the merge; the costliest piece.
+BSA_DEVFN void add_tile(const PackedArgs& a, int c, int ntok, int cand, int& units, int& piece, int& parts) {
+  const int k = max(1, min(a.smax, (c + cand - 1) / cand));
+  units += k;
+  piece = max(piece, (c + k - 1) / k);
+  if (k > 1) parts += k * ntok * a.G;
+}
+BSA_DEVFN float plan_time(const PackedArgs& a, float share, int units, int piece, int parts) {
+  const float unit = piece + kUnitCost;
+  const float merge = (parts > 0 ? kMergeCost : 0.f) +
+                      static_cast<float>(parts) * a.Hkv / (kRowsCost * a.num_sms);
+  // an SM's share of all costs; its share of the units in whole rounds
+  const float even = share + units * kUnitCost / a.num_sms;
+  const float rounds = even * a.num_sms / max(units, 1) * ((units + a.num_sms - 1) / a.num_sms);
+  return merge + (units <= a.num_sms ? unit : max(rounds, even + 0.35f * unit));
 }
 
 // One block: lists the units (tile, split of its keys) of one kv head, longest first.
@@ -265,36 +301,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) 
     atomicMax(&longest, top);
   }
   __syncthreads();
-  // Without splits the SMs are evenly loaded where there are several units for each SM and the
-  // costliest (started first) is no more than an SM's share. Else the cost that a unit may have
-  // is searched, a warp for each candidate: the time is the costliest unit's where every unit
-  // has an SM of its own, and otherwise the units in whole rounds of the SMs, and no less than an
-  // SM's share of all costs and a third of the costliest (SMs are not equally fast).
-  // A unit costs kUnitCost besides its steps, a merge kMergeCost and as much as a step for each
-  // kRowsCost partial rows that are written and read again.
   const float share = static_cast<float>(work) * a.Hkv / a.num_sms;
   int limit = 1 << 30;
   if (a.smax > 1 && ntiles <= kPlanTiles &&
       !(static_cast<float>(longest) <= share && static_cast<long long>(ntiles) * a.Hkv >= 3ll * a.num_sms)) {
-    const int cand = warp == 0 ? 1 << 30 : max(4, static_cast<int>(share * (0.1f + 0.06f * warp)) + 1);
-    int units = 0, piece = 0, parts = 0;        // parts: rows that go through the merge
-    for (int t = lane; t < ntiles; t += 32) {
-      const int c = costs[t] & 0xfffff;
-      const int k = max(1, min(a.smax, (c + cand - 1) / cand));
-      units += k;
-      piece = max(piece, (c + k - 1) / k);
-      if (k > 1 || a.partial) parts += k * (costs[t] >> 20) * a.G;
-    }
+    const int cand = candidate(warp, share);    // a warp for each
+    int units = 0, piece = 0, parts = 0;
+    for (int t = lane; t < ntiles; t += 32)
+      add_tile(a, costs[t] & 0xfffff, costs[t] >> 20, cand, units, piece, parts);
     units = __reduce_add_sync(0xffffffffu, units) * a.Hkv;
     parts = __reduce_add_sync(0xffffffffu, parts);
     piece = __reduce_max_sync(0xffffffffu, piece);
-    const float unit = piece + kUnitCost;
-    const float merge = (parts > 0 && !a.partial ? kMergeCost : 0.f) +
-                        static_cast<float>(parts) * a.Hkv / (kRowsCost * a.num_sms);
-    // an SM's share of all costs; its share of the units in whole rounds
-    const float even = share + units * kUnitCost / a.num_sms;
-    const float rounds = even * a.num_sms / max(units, 1) * ((units + a.num_sms - 1) / a.num_sms);
-    const float time = merge + (units <= a.num_sms ? unit : max(rounds, even + 0.35f * unit));
+    const float time = plan_time(a, share, units, piece, parts);
     if (lane == 0) atomicMin(&best, (static_cast<unsigned long long>(__float_as_uint(time)) << 32) |
                                         static_cast<unsigned>(cand));
     __syncthreads();
@@ -314,7 +332,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) 
     any |= n > 1;
     atomicAdd(&bucket[bucket_of(x, n)], n);
   }
-  any = __syncthreads_or(any) || a.partial;
+  any = __syncthreads_or(any);
   // exclusive sums of the buckets (kBuckets <= kPlanThreads)
   int mine = tid < kBuckets ? bucket[tid] : 0, x = mine;
 #pragma unroll
@@ -352,6 +370,263 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) 
   }
 }
 
+// The plan of few tiles (at most 32 of as many sequences, and no more for all kv heads than SMs)
+// by every block's loader warp for itself, a lane a sequence and then a tile: at most two units a
+// block, the first round of them from the costliest down, the second back from the last block to
+// the first. The block's entries go to own[], the number of all units is returned. The block of a
+// tile's first unit writes its rows' number of splits, block 0 those of rows of no sequence.
+// One row over ten keys takes 9.3 us instead of 13.0 with the plan kernel, 32 rows behind 32K keys
+// 49 instead of 56; with 84 units to cut (648 rows over 16K keys, d = 64) 165 and 168.
+BSA_DEVFN int plan_in_warp(const PackedArgs& a, int4* own) {
+  constexpr unsigned kAll = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  const int per = packed_unit_tokens(a.G), half = per / 2;
+  const bool first_block = blockIdx.x == 0;
+  auto sum_up = [&](int x) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kAll, x, o);
+      if (lane >= o) x += y;
+    }
+    return x;
+  };
+  // how many lanes' sums are at most t, which is less than the last
+  auto find = [&](int sums, int t) {
+    int lo = 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      if (__shfl_sync(kAll, sums, lo + o - 1) <= t) lo += o;
+    return lo;
+  };
+  int first = 0, last = 0, len = 0;
+  bool bad = false, wrong = false;
+  if (lane < a.B) {
+    first = seq_first(a, lane);
+    last = seq_first(a, lane + 1);
+    len = a.seq_lens != nullptr ? a.seq_lens[lane] : a.T;
+    bad = first < 0 || last < first || last > a.N || (lane == 0 && first != 0);
+    wrong = bad || len < 0 || len > a.T || (a.causal && len < last - first);
+    len = max(0, min(len, a.T));
+  }
+  if (wrong && first_block) report(a.status, BSA_DEV_BAD_LENGTH);
+  if (__any_sync(kAll, bad)) first = last = 0;
+  const int end = __shfl_sync(kAll, last, a.B - 1);
+  const int tiles = (last - first + per - 1) / per, sums = sum_up(tiles);
+  const int ntiles = __shfl_sync(kAll, sums, 31);
+  int n = 0, c = 0;
+  Tile x = {};
+  {
+    const int b = find(sums, lane);    // lanes from ntiles on: any
+    const int row = __shfl_sync(kAll, first, b), count = __shfl_sync(kAll, last, b) - row;
+    const int i = (lane - __shfl_sync(kAll, sums - tiles, b)) * per;
+    const int length = __shfl_sync(kAll, len, b);
+    if (lane < ntiles) {
+      const int ntok = min(per, count - i), pos0 = length - count + i;
+      const int keys = a.causal ? max(0, min(length, pos0 + ntok)) : length;
+      x = {b, row + i, ntok, pos0, length, (keys + kStep - 1) / kStep};
+      c = ntok > half ? 2 * x.steps : x.steps;
+      n = 1;
+    }
+  }
+  if (a.smax > 1) {
+    const float share = static_cast<float>(__reduce_add_sync(kAll, c)) * a.Hkv / a.num_sms;
+    const int cand = candidate(lane, share);
+    int units = 0, piece = 0, parts = 0;
+    for (int t = 0; t < ntiles; ++t)
+      add_tile(a, __shfl_sync(kAll, c, t), __shfl_sync(kAll, x.ntok, t), cand, units, piece, parts);
+    units *= a.Hkv;
+    const float time = units <= 2 * a.num_sms ? plan_time(a, share, units, piece, parts) : INFINITY;
+    const unsigned best = __reduce_min_sync(kAll, __float_as_uint(time));
+    const int limit = __shfl_sync(kAll, cand, __ffs(__ballot_sync(kAll, __float_as_uint(time) == best)) - 1);
+    if (lane < ntiles) n = max(1, min(min(a.smax, x.steps), (c + limit - 1) / limit));
+  }
+  // units of costlier pieces, and of equal ones before this one, come first
+  const int piece = n > 0 ? (c + n - 1) / n : -1;
+  int at = 0, entries = 0;
+  for (int t = 0; t < ntiles; ++t) {
+    const int p = __shfl_sync(kAll, piece, t), m = __shfl_sync(kAll, n, t);
+    if (p > piece || (p == piece && t < lane)) at += m;
+    entries += m;
+  }
+  const bool any = __any_sync(kAll, n > 1);
+  if (first_block) {
+    if (any)
+      for (int r = end + lane; r < a.N; r += 32) a.row_splits[r] = 0;
+    if (lane == 0) a.head[2] = any ? 1 : 0;
+  }
+  const int units = entries * a.Hkv;
+  for (int k = 0; k < 2; ++k) {
+    const int u = k == 0 ? blockIdx.x : 2 * gridDim.x - 1 - blockIdx.x;
+    if (u >= units) break;
+    const int e = u / a.Hkv;
+    const bool mine = n > 0 && at <= e && e < at + n;
+    if (mine) {
+      const int split = e - at;
+      own[2 * k] = make_int4(x.b, x.row0, x.ntok, x.pos0);
+      own[2 * k + 1] = make_int4(x.len, x.steps * split / n, x.steps * (split + 1) / n, split | (n << 16));
+      if (any && split == 0 && u % a.Hkv == 0)
+        for (int i = 0; i < x.ntok; ++i) a.row_splits[x.row0 + i] = n;
+    }
+  }
+  __syncwarp();
+  return units;
+}
+
+// ------------------------------------------------------------------------------- results
+// 32 bytes, in one store where `wide` (aligned to 32): lanes that write rows far apart fill whole
+// sectors.
+BSA_DEVFN void store32(void* p, const uint32_t (&v)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// Four warps write the units' results while the softmax warps are at the next unit: thread r of
+// them has row r of a tile, 16 columns at a time.
+template <int D>
+BSA_DEVFN void out_role(const PackedArgs& a, Bars* bars, uint32_t tmem) {
+  const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
+  const int row = quarter * 32 + lane, half_tok = 128 >> a.lgG;
+  const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+  const bool wide = ((reinterpret_cast<uintptr_t>(a.o) | reinterpret_cast<uintptr_t>(a.o_f32)) & 31) == 0;
+  uint32_t un = 0, ml_phase = 0, o_phase = 0;      // o_phase: a bit for each tile
+  bool ok = true;
+  while (ok) {
+    const int slot = un & 1;
+    if (!warp_sleep_all(&bars->info_full[slot], (un >> 1) & 1)) break;
+    ++un;
+    const volatile Unit& U = bars->info[slot];
+    if (U.u < 0 || aborted(bars)) return;
+    const int steps = U.step1 - U.step0;
+    const bool empty = steps <= 0, one = U.ntok <= half_tok;
+    // One tile of rows: its steps were taken by both tiles of tensor memory, or by the first.
+    const bool two = one && steps > 1;
+    for (int t = 0; t < (one ? 1 : 2) && ok; ++t) {
+      const int tok = t * half_tok + (row >> a.lgG);
+      const bool live = tok < U.ntok, part = U.nsplit > 1;
+      const int64_t at = (static_cast<int64_t>(U.row0) + tok) * a.Hq + U.g * a.G + (row & (a.G - 1));
+      const bool join = live && !part && a.lse_own != nullptr;
+      float w = -INFINITY;                     // o_own is on its way while the unit runs
+      if (join) {
+        w = a.lse_own[at] * kLog2e;
+        for (int c = 0; c < D; c += 32) prefetch_l1(a.o_own + at * D + c);
+      }
+      float m = -INFINITY, L = 0.f, f0 = 1.0f, f1 = 0.0f;
+      if (!empty) {
+        ok = warp_sleep_all(&bars->ml_full[t], ml_phase) && warp_sleep_all(&bars->o_full[t], (o_phase >> t) & 1);
+        o_phase ^= 1u << t;
+        if (ok && one) ok = warp_sleep_all(&bars->ml_full[1], ml_phase);
+        if (ok && two) {
+          ok = warp_sleep_all(&bars->o_full[1], o_phase >> 1);
+          o_phase ^= 2u;
+        }
+        if (!ok) break;
+        tc::fence_after_sync();
+        const float2 x = bars->ml[t][row];
+        m = x.x;
+        L = x.y;
+        if (two) {
+          const float2 x1 = bars->ml[1][row];
+          m = fmaxf(x.x, x1.x);
+          const float base = m == -INFINITY ? 0.f : m;
+          f0 = ex2(x.x - base);
+          f1 = ex2(x1.x - base);
+          L = x.y * f0 + x1.y * f1;
+        }
+      }
+      float own = 0.f;                         // weight of o_own, which is normalised
+      if (w != -INFINITY) {
+        const float top = fmaxf(m, w), base = top == -INFINITY ? 0.f : top;
+        const float f = ex2(m - base);
+        own = ex2(w - base);
+        L = L * f + own;
+        f0 *= f;
+        f1 *= f;
+        m = top;
+      }
+      if (!part) {
+        const float inv = L == 0.f ? 0.f : 1.0f / L;
+        f0 *= inv;
+        f1 *= inv;
+        own *= inv;
+      }
+      const int64_t pat = static_cast<int64_t>(U.split) * a.N * a.Hq + at;
+      float* of = part ? a.part_o + pat * D : a.o_f32 != nullptr ? a.o_f32 + at * D : nullptr;
+      if (live) {
+        if (part)
+          *reinterpret_cast<float2*>(a.part_ml + 2 * pat) = make_float2(m, L);
+        else
+          a.lse[at] = L == 0.f ? -INFINITY : (m + log2f(L)) * kLn2;
+      }
+      const uint32_t o_tm = tmem + lane_addr + 128 * t;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 16) {
+        __syncwarp();
+        float v[16];
+        if (empty) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = 0.f;
+        } else {
+          uint32_t x[16];
+          ld16(o_tm + c, x);
+          tc::wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(x[i]) * f0;
+          if (two) {
+            ld16(o_tm + 128 + c, x);
+            tc::wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = fmaf(__uint_as_float(x[i]), f1, v[i]);
+          }
+        }
+        if (c + 16 == D && !empty) {           // the last of O is read
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bars->o_empty[t]);
+            if (one) mbar_arrive(&bars->o_empty[1]);
+          }
+        }
+        if (live && own != 0.f) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 y = *reinterpret_cast<const float4*>(a.o_own + at * D + c + 4 * i);
+            v[4 * i] = fmaf(y.x, own, v[4 * i]);
+            v[4 * i + 1] = fmaf(y.y, own, v[4 * i + 1]);
+            v[4 * i + 2] = fmaf(y.z, own, v[4 * i + 2]);
+            v[4 * i + 3] = fmaf(y.w, own, v[4 * i + 3]);
+          }
+        }
+        if (live && of != nullptr) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[8 * h + i]);
+            store32(of + c + 8 * h, w, wide || part);
+          }
+        }
+        if (live && !part) {
+          uint32_t w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+          store32(static_cast<__nv_bfloat16*>(a.o) + at * D + c, w, wide);
+        }
+      }
+    }
+    if (!ok) break;
+    if (!empty) ml_phase ^= 1;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->info_empty[slot]);
+  }
+  if (lane == 0) set_abort(bars, a.status);
+}
+
 // ------------------------------------------------------------------------------- main
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -372,14 +647,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars->info_full[x], 1);
-      mbar_init(&bars->info_empty[x], 3 + kSoftmaxWarps);   // with the issuer, patch and Q warps
+      mbar_init(&bars->info_empty[x], 7 + kSoftmaxWarps);   // with the issuer, patch, Q, out warps
       mbar_init(&bars->q_full[x], 1);
       mbar_init(&bars->q_empty[x], 1);
       mbar_init(&bars->s_full[x], 1);
       mbar_init(&bars->p_ready[x][0], 4);    // the tile's softmax warps
       mbar_init(&bars->p_ready[x][1], 4);
-      mbar_init(&bars->pair[2 * x], 2);
-      mbar_init(&bars->pair[2 * x + 1], 2);
+      mbar_init(&bars->ml_full[x], 4);
+      mbar_init(&bars->o_empty[x], 4);       // the out warps
       mbar_init(&bars->o_full[x], 1);
     }
     mbar_init(&bars->mma_done, 1);
@@ -406,22 +681,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   grid_launch_dependents();            // the merge kernel may be set up, and waits for this one
   grid_dependency_wait();
+  int own_units = 0;                   // (before the registers are shared out: it takes more)
+  if (a.in_block && warp == kWarpLoad) own_units = plan_in_warp(a, bars->own);
 
-  if (warp >= kSoftmaxWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (warp >= kWarpOut) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRegsOut));
+    out_role<D>(a, bars, tmem);
+  } else if (warp >= kSoftmaxWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRegsOther));
     if (warp == kWarpLoad) {
       // ------------------------------------------------------------------ units, K, V
       uint32_t un = 0, kc = 0;
-      bool ok = true, taken = false;
-      int next = 0;
-      int entries = 0;
+      bool ok = true;
+      int next = 0, units = 0;
       while (ok) {
         const int slot = un & 1;
         Unit U = {-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-        int u = blockIdx.x;            // the first unit; the others come from the counter
-        if (taken) {
-          u = static_cast<int>(gridDim.x) + __shfl_sync(0xffffffffu, next, 0);
-        }
+        // the first unit; the others come from the counter
+        int u = blockIdx.x;
+        if (un > 0) u = a.in_block ? 2 * gridDim.x - 1 - blockIdx.x
+                                   : gridDim.x + __shfl_sync(0xffffffffu, next, 0);
         // The heads of an entry are neighbours: the longest units of all heads start first
         // (prompts of 2K and 4K: 53 and 146 us, 69 and 168 with one head after the other), and
         // an entry is read beside the number of entries. Without the causal limit units are
@@ -429,13 +708,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the units at work share its keys through L2 (200 rows behind three prefixes of up to
         // 64K: 399 us, 437 with the heads as neighbours).
         int e = min(u / a.Hkv, a.max_entries - 1), g = u % a.Hkv;
-        int4 e0 = a.entries[2 * e], e1 = a.entries[2 * e + 1];
-        if (!taken) entries = a.head[0];
-        taken = true;
-        const int units = entries * a.Hkv;
-        if (!a.causal && units > static_cast<int>(gridDim.x) && u < units) {
-          g = u / entries;
-          e = u - g * entries;
+        const int4* from = a.in_block ? bars->own + 2 * (un & 1) : a.entries + 2 * e;
+        int4 e0 = from[0], e1 = from[1];
+        if (un == 0) units = a.in_block ? own_units : a.head[0] * a.Hkv;
+        if (un == 2 && a.in_block) units = 0;
+        if (!a.causal && !a.in_block && units > static_cast<int>(gridDim.x) && u < units) {
+          g = u / (units / a.Hkv);
+          e = u - g * (units / a.Hkv);
           e0 = a.entries[2 * e];
           e1 = a.entries[2 * e + 1];
         }
@@ -495,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         if (!ok || U.u < 0 || aborted(bars)) break;
         ++un;
-        if (U.step1 <= U.step0 && lane == 0) next = atomicAdd(&a.head[1], 1);
+        if (U.step1 <= U.step0 && lane == 0 && !a.in_block) next = atomicAdd(&a.head[1], 1);
         for (int s0 = U.step0; s0 < U.step1 && ok; s0 += 16) {
           if (s0 > U.step0) look_up(2 * s0);
           const int n_here = min(16, U.step1 - s0);
@@ -505,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
               // the next unit, shortly before this one's copies end: not earlier, since a unit
               // waits while its block is busy
-              if (s0 + q == max(U.step1 - 3, U.step0)) next = atomicAdd(&a.head[1], 1);
+              if (s0 + q == max(U.step1 - 3, U.step0) && !a.in_block) next = atomicAdd(&a.head[1], 1);
               // a step that has the sequence's end or a bad block goes through the patch warp
               const bool patch = (s0 + q + 1) * kStep > U.len || k0 < 0 || k1 < 0;
               for (int kv = 0; kv < 2 && ok; ++kv, ++kc) {
@@ -628,7 +907,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dq0 = tc::smem_desc_sw128(sbase, 16, 1024);
       const uint64_t dk0 = tc::smem_desc_sw128(sbase + C::kOffKV, 16, 1024);
       const uint64_t dv0 = tc::smem_desc_sw128(sbase + C::kOffKV, C::kSlab, 1024);
-      uint32_t un = 0, q_phase = 0, p_phase = 0;   // a bit for each tile
+      uint32_t un = 0, q_phase = 0, p_phase = 0;   // phases: a bit for each tile
+      uint32_t o_phase = 1;                        // of o_empty, at the unit before
       struct Pos {                                 // a stage of the ring and its phase
         int st;
         uint32_t phase;
@@ -676,6 +956,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t phase = (p_phase >> t) & 1;
         p_phase ^= 1u << t;
         const uint64_t dv = dv0 + ((p.st * C::kTile) >> 4);
+        if (first && !mbar_wait(&bars->o_empty[t], o_phase)) return false;
         if (!mbar_wait(&bars->p_ready[t][0], phase) || !full(p)) return false;
         tc::fence_after_sync();
 #pragma unroll
@@ -739,6 +1020,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+        o_phase ^= 1;
         if (ok) ok = fetch();
       }
       if (!ok) set_abort(bars, a.status);
@@ -750,22 +1032,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ softmax of tile t
     // Warp w has rows 32 (w % 4) .. + 31 of the tile (the quarter of tensor memory that it
     // reaches), one a thread: row maxima and sums need no exchange.
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kRegsSoftmax));
     const int t = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_col = tmem + lane_addr + 256 + 128 * t;
     const float sc = a.scale_log2;
-    uint64_t* pair = &bars->pair[quarter];
-    // barrier phases, a bit each: 0-1 o_full of the tiles, 2 pair, 3 s_full, 4-5 units mod 4
-    uint32_t bits = 0;
-    // the warps of these rows in both tiles have come here
-    auto meet = [&]() {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(pair);
-      bits ^= 4;
-      return warp_wait_all(pair, ((bits >> 2) & 1) ^ 1);
-    };
+    // barrier phases, a bit each: 0 o_empty, at the unit before, 3 s_full, 4-5 units mod 4
+    uint32_t bits = 1;
     while (true) {
       const int slot = (bits >> 4) & 1;
       if (!warp_sleep_all(&bars->info_full[slot], (bits >> 5) & 1)) {
@@ -884,100 +1158,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) set_abort(bars, a.status);
         break;
       }
-      // ---- epilogue: a thread writes its row or, with one tile of rows, half of it
-      const bool empty = U.step1 <= U.step0;
-      const bool one = U.ntok <= half_tok, twin = one && !empty;
-      const bool both = !one || U.step1 - U.step0 > 1;   // tile 1 had steps too
-      const int tok = (one ? 0 : t * half_tok) + row / a.G, hh = row % a.G;
-      const bool live = tok < U.ntok;
-      const uint32_t phases = bits;
-      if (!empty) bits ^= both ? 3u : 1u;
-      auto done = [&]() {
+      // (m, l) goes to the out warps, which have read the last unit's
+      if (U.step1 > U.step0) {
+        if (!warp_wait_all(&bars->o_empty[t], bits & 1)) {
+          if (lane == 0) set_abort(bars, a.status);
+          break;
+        }
+        bits ^= 1;
+        bars->ml[t][row] = make_float2(m, l.x + l.y);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->info_empty[slot]);
-      };
-      if (idle || (t == 1 && one && empty)) {
-        done();
-        continue;
+        if (lane == 0) mbar_arrive(&bars->ml_full[t]);
       }
-      float L = l.x + l.y;
-      if (twin) {
-        bars->swap[t][row] = make_float2(m, L);
-        ok = meet();
-      }
-      if (ok && !empty) {
-        if (twin || t == 0) ok = warp_sleep_all(&bars->o_full[0], phases & 1);
-        if (ok && both && (twin || t == 1)) ok = warp_sleep_all(&bars->o_full[1], (phases >> 1) & 1);
-      }
-      if (!ok) {
-        if (lane == 0) set_abort(bars, a.status);
-        break;
-      }
-      tc::fence_after_sync();
-      float f0 = 1.0f, f1 = 0.0f;     // weights of the two tiles' O
-      if (twin) {
-        const float2 x0 = bars->swap[0][row], x1 = bars->swap[1][row];
-        m = fmaxf(x0.x, x1.x);
-        const float base = m == -INFINITY ? 0.f : m;
-        f0 = ex2(x0.x - base);
-        f1 = ex2(x1.x - base);
-        L = x0.y * f0 + x1.y * f1;
-      }
-      const bool part = U.nsplit > 1 || a.partial;
-      const float inv = part ? 1.0f : L == 0.f ? 0.f : 1.0f / L;
-      f0 *= inv;
-      f1 *= inv;
-      const int64_t at = (static_cast<int64_t>(U.row0) + tok) * a.Hq + U.g * a.G + hh;
-      const int64_t pat = static_cast<int64_t>(U.split) * a.N * a.Hq + at;
-      const uint32_t o_first = tmem + lane_addr + (twin ? 0 : 128 * t);
-      const int col0 = twin ? t * (D / 2) : 0, col1 = twin ? col0 + D / 2 : D;
-#pragma unroll 1
-      for (int c = col0; c < col1; c += 32) {
-        float v[32];
-        if (empty) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.f;
-        } else {
-          uint32_t ov[32], ow[32];
-          tc::ld32(o_first + c, ov);
-          if (twin && both) tc::ld32(o_first + 128 + c, ow);
-          tc::wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            v[i] = __uint_as_float(ov[i]) * f0;
-            if (twin && both) v[i] = fmaf(__uint_as_float(ow[i]), f1, v[i]);
-          }
-        }
-        if (live) {
-          if (!part) {
-            uint4* ob = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + at * D + c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              ob[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                                 pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
-          }
-          float* of = part ? a.part_o + pat * D + c : a.o_f32 != nullptr ? a.o_f32 + at * D + c : nullptr;
-          if (of != nullptr) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              reinterpret_cast<float4*>(of)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          }
-        }
-      }
-      if (live && (!twin || t == 0)) {
-        if (part)
-          *reinterpret_cast<float2*>(a.part_ml + 2 * pat) = make_float2(m, L);
-        else
-          a.lse[at] = L == 0.f ? -INFINITY : (m + log2f(L)) * kLn2;
-      }
-      tc::fence_before_sync();
-      const bool wait = twin;
-      done();
-      // both tiles' O and the swap have been read before the next unit writes them
-      if (wait && !meet()) {
-        if (lane == 0) set_abort(bars, a.status);
-        break;
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->info_empty[slot]);
     }
   }
 
@@ -1002,7 +1195,7 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(const PackedArgs a) {
   const int64_t at = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   if (at >= static_cast<int64_t>(a.N) * a.Hq) return;
   const int n = a.row_splits[at / a.Hq];
-  if (n == 0 || (n == 1 && !a.partial)) return;
+  if (n <= 1) return;
   const int64_t rows = static_cast<int64_t>(a.N) * a.Hq;
   const float own = a.lse_own != nullptr ? a.lse_own[at] * kLog2e : -INFINITY;
   float M = own;
@@ -1080,7 +1273,8 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(const PackedArgs a) {
 template <int D>
 cudaError_t launch_d(const PackedArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
                      const CUtensorMap& tv, int num_sms, cudaStream_t s) {
-  cudaError_t e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a);
+  cudaError_t e = cudaSuccess;
+  if (!a.in_block) e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a);
   if (e != cudaSuccess) return e;
   constexpr int smem = smem_bytes<D>();
   auto kern = packed_attn_kernel<D>;
@@ -1089,7 +1283,7 @@ cudaError_t launch_d(const PackedArgs& a, const CUtensorMap& tq, const CUtensorM
   const int64_t units = static_cast<int64_t>(a.max_entries) * a.Hkv;
   const int grid = static_cast<int>(units < num_sms ? units : num_sms);
   e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s, a, tq, tk, tv);
-  if (e != cudaSuccess || (a.smax == 1 && !a.partial)) return e;
+  if (e != cudaSuccess || a.smax == 1) return e;
   const int64_t warps = static_cast<int64_t>(a.N) * a.Hq;
   return launch_pdl(packed_merge_kernel<D>, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0, s, a);
 }

@@ -35,7 +35,7 @@ struct PackedArgs {
   CacheView k, v;
   const int32_t* cu;          // [B+1] or null
   const int32_t* seq_lens;    // [B] or null
-  const float* o_own;         // [N, Hq, d] or null: joined by the merge
+  const float* o_own;         // [N, Hq, d] or null: joined by who writes the row
   const float* lse_own;       // [N, Hq]
   void* o;                    // [N, Hq, d] bf16
   float* lse;                 // [N, Hq]
@@ -47,7 +47,8 @@ struct PackedArgs {
   int32_t* row_splits;        // plan: [N] partial results of each row (0: row not written)
   float* part_ml;             // [smax, N, Hq, 2] (max, sum) in log2 units
   float* part_o;              // [smax, N, Hq, d] fp32, not normalised
-  int N, B, Hq, Hkv, G, d, T, causal, smax, partial;   // partial: every row goes through part_*
+  int N, B, Hq, Hkv, G, d, T, causal, smax;
+  int in_block;               // few tiles: every block plans for itself
   int max_entries, num_sms, lgG;   // lgG: log2(G)
   int k_safe, v_safe;         // every page (or block) of the cache lies inside its extent
   float scale_log2;

@@ -520,3 +520,85 @@ def test_prompt_append_attend_then_shared_decode():
             for a, y in zip(want, r):
                 a[b, h] = y[0]
     check(shared, want, doc + max(lens), d)
+
+
+# ------------------------------------------------------------------ both ways to plan
+PLANS = [
+    # new, lens, Hkv, G, d, causal
+    ([1] * 31, [1 + 83 * b for b in range(31)], 2, 4, 128, True),      # a block plans for itself
+    ([1] * 32, [1 + 83 * b for b in range(32)], 2, 4, 128, True),      # 33 tiles: the plan kernel
+    ([2] * 40, [2600 - 64 * b for b in range(40)], 1, 4, 64, False),
+    ([800], [2900], 4, 8, 64, True),           # 25 tiles of 4 heads, cut: two units a block
+    ([800], [2900], 4, 8, 64, False),
+    ([600], [1500], 37, 1, 64, True),          # at most 4 tiles of 37 heads: as many as SMs
+    ([600], [1500], 38, 1, 64, True),
+    ([33, 0, 65, 1], [1600, 0, 1537, 1], 3, 4, 128, True),
+]
+
+
+@pytest.mark.parametrize("new,lens,Hkv,G,d,causal", PLANS)
+def test_units_of_both_plans(new, lens, Hkv, G, d, causal):
+    cu = sums(new)
+    mem = Paged(lens, Hkv, d, seed=90)
+    q = randn(cu[-1] + 2, Hkv * G, d, seed=91, scale=1.5)
+    step = run_attend(q, mem, cu, lens, Hkv, causal)
+    check(step, exact(q, mem, cu, lens, causal, G), max(lens), d)
+
+
+@pytest.mark.parametrize("B", [3, 40])
+@pytest.mark.parametrize("T", [128, 4096])
+def test_bad_ranges_are_refused_by_both_plans(B, T):
+    mem = Paged([100] * B, 1, 64, seed=92, T=T)
+    q = randn(3 * B, 2, 64, seed=93)
+    good = list(range(0, 3 * B + 1, 3))
+    tok = bsa.Tokens(N=3 * B, B=B, Hq=2, Hkv=1, d=64, T=T, cu_seqlens=ints(good),
+                     seq_lens=ints([100] * B))
+    step = bsa.PackedAttention(tok)
+    step.run(q, *mem.caches())                   # leaves results in the workspace
+    assert int(step.status.item()) == 0
+    for at, value in ((0, 1), (1, 0x7fffffff), (1, -2147483648), (B - 1, 0), (B, 3 * B + 1)):
+        cu = list(good)
+        cu[at] = value
+        tok.cu_seqlens = ints(cu)
+        step.status.zero_()
+        for x in (step.o, step.lse, step.o_f32):
+            x.fill_(77.0)
+        step.run(q, *mem.caches())
+        assert int(step.status.item()) == bsa.BSA_DEV_BAD_LENGTH
+        assert all((x == 77.0).all() for x in (step.o, step.lse, step.o_f32))
+
+
+@pytest.mark.parametrize("n", [100, 1500])
+def test_outputs_that_start_at_16_bytes(n):
+    """32-byte stores are for outputs on 32-byte boundaries."""
+    d, G, Hkv = 128, 4, 2
+    mem = Paged([n], Hkv, d, seed=94)
+    q = randn(70, Hkv * G, d, seed=95)
+    want = run_attend(q, mem, [0, 70], [n], Hkv)
+    size = 70 * Hkv * G * d
+    o = torch.zeros(size + 8, dtype=torch.bfloat16, device="cuda")[8:].view(70, Hkv * G, d)
+    o_f32 = torch.zeros(size + 4, device="cuda")[4:].view(70, Hkv * G, d)
+    lse = torch.zeros(70, Hkv * G, device="cuda")
+    for a, b in ((o, want.o_f32), (want.o, o_f32), (o, o_f32), (o, None)):
+        for x in (o, o_f32, lse):
+            x.zero_()
+        b = torch.empty_like(want.o_f32) if b is want.o_f32 else b
+        a = torch.empty_like(want.o) if a is want.o else a
+        bsa.bsa_attend_packed(want.tok, q, *mem.caches(), a, lse, b, want.workspace, want.status)
+        assert torch.equal(a, want.o) and torch.equal(lse, want.lse)
+        assert b is None or torch.equal(b, want.o_f32)
+
+
+@pytest.mark.parametrize("lens", [[100, 0, 64], [5000, 0, 300]])
+@pytest.mark.parametrize("rows", [[2, 1, 40], [70, 3, 300]])
+def test_the_own_part_is_joined_once(rows, lens):
+    """By the unit that has a row alone, or by the merge of its splits."""
+    d, G, Hkv = 128, 4, 2
+    cu = sums(rows)
+    mem = Paged(lens, Hkv, d, seed=96)
+    q = randn(cu[-1] + 1, Hkv * G, d, seed=97, scale=1.5)
+    own = (torch.randn(cu[-1] + 1, Hkv * G, d, generator=gen(98), device="cuda"),
+           8.0 + torch.randn(cu[-1] + 1, Hkv * G, generator=gen(99), device="cuda"))
+    own[1][0, :2], own[1][cu[1], :] = 200.0, -math.inf
+    step = run_shared(q, mem, cu, lens, Hkv, own)
+    check(step, exact_shared(q, mem, cu, lens, G, own), max(lens), d)
