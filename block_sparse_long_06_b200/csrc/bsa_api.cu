@@ -298,13 +298,15 @@ PackedWorkspace packed_workspace(const bsa_tokens_t* t, int num_sms) {
   const int64_t rows = t->N > 0 ? t->N : 1;
   const int64_t least = (rows + per - 1) / per;
   const int64_t want = (4ll * num_sms + least * t->Hkv - 1) / (least * t->Hkv);
+  // the most tiles that N rows of up to B sequences can make
+  const int64_t seqs = std::min<int64_t>(rows, t->B), most = seqs + (rows - seqs) / per;
   const int64_t steps = (t->T + 127) / 128;
   w.smax = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, 64), steps)));
   // A merge costs as much as 6 steps of one tile: halving 12 of them gains nothing, and without
   // splits no merge is launched (4 rows behind 1,024 keys: 16 us, 20 with a merge that finds
   // nothing to do).
   if (steps * (t->N > per / 2 ? 2 : 1) <= 12) w.smax = 1;
-  w.max_entries = static_cast<int>((least + std::min<int64_t>(rows, t->B)) * w.smax);
+  w.max_entries = static_cast<int>(most * w.smax);
   w.offs = 256;
   w.entries = w.offs + align256((static_cast<size_t>(t->B) + 1) * sizeof(int32_t));
   w.row_splits = w.entries + align256(static_cast<size_t>(w.max_entries) * 2 * sizeof(int4));
@@ -399,8 +401,8 @@ bsa_status_t packed_attention(const bsa_tokens_t* t, bool shared, const void* q,
   a.smax = w.smax;
   a.max_entries = w.max_entries;
   a.num_sms = num_sms;
+  // plan_in_warp has the reason. With more tiles than SMs, two rounds of units would be too coarse.
   const int max_tiles = w.max_entries / w.smax;
-  // (plan_in_warp has the reason and what it measured)
   a.in_block = t->B <= 32 && max_tiles <= 32 && max_tiles * t->Hkv <= num_sms;
   while ((1 << a.lgG) < a.G) ++a.lgG;
   a.k_safe = inside_extent(k, t);

@@ -53,6 +53,7 @@ static_assert(2 * kRegsSoftmax + kRegsOther + kRegsOut <= 65536 / 128, "register
 constexpr uint32_t kTmemCols = 512;
 constexpr int kStep = 128;             // keys a step
 constexpr int kMaxStages = 10;
+constexpr int kRounds = 2;              // units a block may have where it plans for itself
 constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 512, kPlanTiles = 1024, kPlanSeqs = 1024;
 constexpr float kUnitCost = 4.f, kMergeCost = 6.f, kRowsCost = 64.f;   // in steps of one tile
@@ -83,7 +84,7 @@ struct Bars {
   uint64_t mma_done;
   float2 ml[2][128];                   // [tile][row]
   Unit info[2];
-  int4 own[4];                         // the block's two entries, where it plans for itself
+  int4 own[2 * kRounds];               // the block's entries, where it plans for itself
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -370,13 +371,20 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) 
   }
 }
 
+// the unit that a block which plans for itself takes in round k
+BSA_DEVFN int unit_of_round(int k) {
+  return k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
 // The plan of few tiles (at most 32 of as many sequences, and no more for all kv heads than SMs)
-// by every block's loader warp for itself, a lane a sequence and then a tile: at most two units a
-// block, the first round of them from the costliest down, the second back from the last block to
+// by every block's loader warp for itself, a lane a sequence and then a tile: at most kRounds units
+// a block, the first round of them from the costliest down, the second back from the last block to
 // the first. The block's entries go to own[], the number of all units is returned. The block of a
 // tile's first unit writes its rows' number of splits, block 0 those of rows of no sequence.
 // One row over ten keys takes 9.3 us instead of 13.0 with the plan kernel, 32 rows behind 32K keys
-// 49 instead of 56; with 84 units to cut (648 rows over 16K keys, d = 64) 165 and 168.
+// 48 instead of 55, 693 rows over 3K keys (16/8 heads, d = 64) 43 and 47; where units that blocks
+// take when they are free would be better it loses (27 rows each of 16 sequences over 12K keys,
+// 64/4 heads: 122 and 114). Four rounds: 200 rows behind three prefixes 483 us, 378 with two.
 BSA_DEVFN int plan_in_warp(const PackedArgs& a, int4* own) {
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31;
@@ -435,7 +443,7 @@ BSA_DEVFN int plan_in_warp(const PackedArgs& a, int4* own) {
     for (int t = 0; t < ntiles; ++t)
       add_tile(a, __shfl_sync(kAll, c, t), __shfl_sync(kAll, x.ntok, t), cand, units, piece, parts);
     units *= a.Hkv;
-    const float time = units <= 2 * a.num_sms ? plan_time(a, share, units, piece, parts) : INFINITY;
+    const float time = units <= kRounds * a.num_sms ? plan_time(a, share, units, piece, parts) : INFINITY;
     const unsigned best = __reduce_min_sync(kAll, __float_as_uint(time));
     const int limit = __shfl_sync(kAll, cand, __ffs(__ballot_sync(kAll, __float_as_uint(time) == best)) - 1);
     if (lane < ntiles) n = max(1, min(min(a.smax, x.steps), (c + limit - 1) / limit));
@@ -455,16 +463,17 @@ BSA_DEVFN int plan_in_warp(const PackedArgs& a, int4* own) {
     if (lane == 0) a.head[2] = any ? 1 : 0;
   }
   const int units = entries * a.Hkv;
-  for (int k = 0; k < 2; ++k) {
-    const int u = k == 0 ? blockIdx.x : 2 * gridDim.x - 1 - blockIdx.x;
+  for (int k = 0; k < kRounds; ++k) {
+    const int u = unit_of_round(k);
     if (u >= units) break;
-    const int e = u / a.Hkv;
+    const bool by_head = !a.causal && units > static_cast<int>(gridDim.x);
+    const int e = by_head ? u % entries : u / a.Hkv, g = by_head ? u / entries : u % a.Hkv;
     const bool mine = n > 0 && at <= e && e < at + n;
     if (mine) {
       const int split = e - at;
       own[2 * k] = make_int4(x.b, x.row0, x.ntok, x.pos0);
       own[2 * k + 1] = make_int4(x.len, x.steps * split / n, x.steps * (split + 1) / n, split | (n << 16));
-      if (any && split == 0 && u % a.Hkv == 0)
+      if (any && split == 0 && g == 0)
         for (int i = 0; i < x.ntok; ++i) a.row_splits[x.row0 + i] = n;
     }
   }
@@ -699,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Unit U = {-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
         // the first unit; the others come from the counter
         int u = blockIdx.x;
-        if (un > 0) u = a.in_block ? 2 * gridDim.x - 1 - blockIdx.x
+        if (un > 0) u = a.in_block ? unit_of_round(un)
                                    : gridDim.x + __shfl_sync(0xffffffffu, next, 0);
         // The heads of an entry are neighbours: the longest units of all heads start first
         // (prompts of 2K and 4K: 53 and 146 us, 69 and 168 with one head after the other), and
@@ -708,15 +717,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the units at work share its keys through L2 (200 rows behind three prefixes of up to
         // 64K: 399 us, 437 with the heads as neighbours).
         int e = min(u / a.Hkv, a.max_entries - 1), g = u % a.Hkv;
-        const int4* from = a.in_block ? bars->own + 2 * (un & 1) : a.entries + 2 * e;
+        const int4* from = a.in_block ? bars->own + 2 * (un % kRounds) : a.entries + 2 * e;
         int4 e0 = from[0], e1 = from[1];
         if (un == 0) units = a.in_block ? own_units : a.head[0] * a.Hkv;
-        if (un == 2 && a.in_block) units = 0;
-        if (!a.causal && !a.in_block && units > static_cast<int>(gridDim.x) && u < units) {
+        if (un == kRounds && a.in_block) units = 0;
+        if (!a.causal && units > static_cast<int>(gridDim.x) && u < units) {
           g = u / (units / a.Hkv);
           e = u - g * (units / a.Hkv);
-          e0 = a.entries[2 * e];
-          e1 = a.entries[2 * e + 1];
+          if (!a.in_block) {
+            e0 = a.entries[2 * e];
+            e1 = a.entries[2 * e + 1];
+          }
         }
         int rk = -1, rv = -1, nblk = 0;
         // the cache rows of the unit's blocks from `first`, one a lane: -1 behind the end, and
