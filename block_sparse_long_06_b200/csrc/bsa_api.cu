@@ -302,7 +302,7 @@ PackedWorkspace packed_workspace(const bsa_tokens_t* t, int num_sms) {
   const int64_t seqs = std::min<int64_t>(rows, t->B), most = seqs + (rows - seqs) / per;
   const int64_t steps = (t->T + 127) / 128;
   w.smax = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, 64), steps)));
-  // A merge costs as much as 6 steps of one tile: halving 12 of them gains nothing, and without
+  // A merge costs as much as 4 to 6 steps of one tile: halving 12 of them gains little, and without
   // splits no merge is launched (4 rows behind 1,024 keys: 16 us, 20 with a merge that finds
   // nothing to do).
   if (steps * (t->N > per / 2 ? 2 : 1) <= 12) w.smax = 1;

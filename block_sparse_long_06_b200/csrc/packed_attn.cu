@@ -35,6 +35,8 @@
 //    step is handed to the tensor cores. K there may be anything: its scores are replaced.
 // Tensor memory: O of tile t at 128 t, S (and P) of tile t at 256 + 128 t. Every wait is
 // bounded; on a timeout the kernel reports BSA_DEV_TIMEOUT, drains and returns.
+#include <algorithm>
+
 #include "tcgen05.cuh"
 #include "tokens_common.cuh"
 #include "tokens_internal.h"
@@ -48,15 +50,17 @@ constexpr int kWarpOut = 12;           // and 12-15: results
 // of every kPolyOf pairs of a row's scores, kPoly take their exponentials by polynomial
 constexpr int kPolyOf = 8, kPoly = 1;
 // registers a thread of the softmax warps, of the warps 8-11 and of 12-15
-constexpr int kRegsSoftmax = 192, kRegsOther = 64, kRegsOut = 64;
+constexpr int kRegsSoftmax = 192, kRegsOther = 56, kRegsOut = 72;
 static_assert(2 * kRegsSoftmax + kRegsOther + kRegsOut <= 65536 / 128, "registers of the launch");
 constexpr uint32_t kTmemCols = 512;
 constexpr int kStep = 128;             // keys a step
 constexpr int kMaxStages = 10;
 constexpr int kRounds = 2;              // units a block may have where it plans for itself
 constexpr int kPlanThreads = 1024;
+constexpr int kMergeThreads = 256, kMergeBlocks = 4;    // blocks an SM
 constexpr int kBuckets = 512, kPlanTiles = 1024, kPlanSeqs = 1024;
-constexpr float kUnitCost = 4.f, kMergeCost = 6.f, kRowsCost = 64.f;   // in steps of one tile
+// in quarters of a step of two tiles (750 cycles)
+constexpr float kUnitCost = 8.f, kMergeCost = 12.f, kRowsCost = 10.f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -171,15 +175,20 @@ BSA_DEVFN int seq_len(const PackedArgs& a, int b) {
   return a.seq_lens != nullptr ? max(0, min(a.seq_lens[b], a.T)) : a.T;
 }
 
+// What a step of a unit costs: with two tiles of rows it takes 3,010 cycles (d = 64: 2,820), with
+// one 2,290, which its keys take to arrive, and 1,460 at d = 64.
+BSA_DEVFN int step_cost(int d, bool two) { return two ? 4 : d == 128 ? 3 : 2; }
+
 // Without splits the SMs are evenly loaded where there are several units for each SM and the
 // costliest (started first) is no more than an SM's share. Else the cost that a unit may have is
 // searched among 32 candidates. The time with one is the costliest unit's where every unit has an
 // SM of its own, and otherwise the units in whole rounds of the SMs, and no less than an SM's
-// share of all costs and a third of the costliest (SMs are not equally fast). A unit costs
-// kUnitCost besides its steps, a merge kMergeCost and as much as a step for each kRowsCost
-// partial rows that are written and read again.
+// share of all costs and a fifth of the costliest (SMs are not equally fast). A unit costs
+// kUnitCost besides its steps, a merge kMergeCost and 1 for each kRowsCost partial rows of an SM,
+// which are written and read again (with 20 for 10: 20 chunks of up to 241 rows over 9K keys,
+// 32/4 heads, 309 us for 257; with a third for a fifth: 200 rows behind three prefixes 390 for 359).
 BSA_DEVFN int candidate(int i, float share) {
-  return i == 0 ? 1 << 30 : max(4, static_cast<int>(share * (0.1f + 0.06f * i)) + 1);
+  return i == 0 ? 1 << 30 : max(12, static_cast<int>(share * (0.1f + 0.06f * i)) + 1);
 }
 // What a tile of cost c and ntok tokens adds under the candidate: units and the rows (of one kv
 // head) that go through the merge; the costliest piece.
@@ -196,7 +205,7 @@ BSA_DEVFN float plan_time(const PackedArgs& a, float share, int units, int piece
   // an SM's share of all costs; its share of the units in whole rounds
   const float even = share + units * kUnitCost / a.num_sms;
   const float rounds = even * a.num_sms / max(units, 1) * ((units + a.num_sms - 1) / a.num_sms);
-  return merge + (units <= a.num_sms ? unit : max(rounds, even + 0.35f * unit));
+  return merge + (units <= a.num_sms ? unit : max(rounds, even + 0.2f * unit));
 }
 
 // One block: lists the units (tile, split of its keys) of one kv head, longest first.
@@ -284,13 +293,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) 
   Tile own;                            // this thread's first tile: one is all there is, mostly
   if (tid < ntiles) own = tile_of(tid);
   auto tile = [&](int t) { return t == tid ? own : tile_of(t); };
-  // cost of all tiles and of the costliest: a step of two 128-row tiles costs twice a step of one
-  auto cost_of = [&](const Tile& x) { return x.ntok > half ? 2 * x.steps : x.steps; };
+  // cost of all tiles and of the costliest
+  auto cost_of = [&](const Tile& x) { return step_cost(a.d, x.ntok > half) * x.steps; };
   unsigned long long sum = 0;
   int top = 0;
   for (int t = tid; t < ntiles; t += kPlanThreads) {
     const int c = cost_of(tile(t));
-    if (t < kPlanTiles) costs[t] = c | (tile(t).ntok << 20);
+    if (t < kPlanTiles) costs[t] = min(c, 0xfffff) | (tile(t).ntok << 20);
     sum += c;
     top = max(top, c);
   }
@@ -432,7 +441,7 @@ BSA_DEVFN int plan_in_warp(const PackedArgs& a, int4* own) {
       const int ntok = min(per, count - i), pos0 = length - count + i;
       const int keys = a.causal ? max(0, min(length, pos0 + ntok)) : length;
       x = {b, row + i, ntok, pos0, length, (keys + kStep - 1) / kStep};
-      c = ntok > half ? 2 * x.steps : x.steps;
+      c = step_cost(a.d, ntok > half) * x.steps;
       n = 1;
     }
   }
@@ -948,11 +957,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (stop || total > 0) return true;
         }
       };
+      // sums with a descriptor are made where they are used: made ahead, they spill
+      auto keep = [](uint64_t& desc) { asm volatile("" : "+l"(desc)); };
       auto full = [&](const Pos& p) { return mbar_wait(&bars->kv_full[p.st], p.phase); };
       auto release = [&](const Pos& p) { tc::commit(&bars->kv_empty[p.st]); };
       // S of tile t from Q tile q
       auto scores = [&](int t, int q, const Pos& p) {
-        const uint64_t dq = dq0 + ((q * C::kTile) >> 4), dk = dk0 + ((p.st * C::kTile) >> 4);
+        uint64_t dq = dq0 + ((q * C::kTile) >> 4), dk = dk0 + ((p.st * C::kTile) >> 4);
+        keep(dq);
+        keep(dk);
         tc::fence_after_sync();
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
@@ -966,7 +979,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t s_tm = tmem + 256 + 128 * t, o_tm = tmem + 128 * t;
         const uint32_t phase = (p_phase >> t) & 1;
         p_phase ^= 1u << t;
-        const uint64_t dv = dv0 + ((p.st * C::kTile) >> 4);
+        uint64_t dv = dv0 + ((p.st * C::kTile) >> 4);
+        keep(dv);
         if (first && !mbar_wait(&bars->o_empty[t], o_phase)) return false;
         if (!mbar_wait(&bars->p_ready[t][0], phase) || !full(p)) return false;
         tc::fence_after_sync();
@@ -1072,8 +1086,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int left = U.step1 - U.step0 - (stride - 1) * t;
       {
         const int tok0 = stride == 2 ? 0 : t * half_tok, tok = tok0 + (row >> a.lgG);
-        // the last key this row sees
-        const int last = tok >= U.ntok ? -1 : a.causal ? min(U.pos0 + tok, U.len - 1) : U.len - 1;
+        // The last key this row sees. Rows that do not exist are masked like the others: if they
+        // saw nothing, their warp would mask every step (3,900 cycles instead of 3,050 where they
+        // are the rest of a tile). Nobody reads them, whatever they hold.
+        const int last = a.causal ? min(U.pos0 + tok, U.len - 1) : U.len - 1;
         lim = last - (U.step0 + (stride - 1) * t) * kStep;
         idle = tok0 + ((quarter * 32) >> a.lgG) >= U.ntok;
       }
@@ -1194,91 +1210,91 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------------------- merge
-// One warp per (row, head): joins the splits' (o, m, l) and, with o_own, what the row's own
-// tokens gave. The lanes read 32 splits' (m, l) at once; the partial rows are read in 16-byte
-// loads, eight in flight, by 32 or, at d = 64, two times 16 lanes, and added in a fixed order.
+// A warp joins the splits' (o, m, l) of a (row, head) and, with o_own, what the row's own tokens
+// gave. All loads of up to 8 (d = 64: 16) splits are under way before the first is used; a lane
+// holds (m, l) of splits lane and lane + 32 (there are no more than 64), and 16 bytes of the
+// partial rows, which 32 or, at d = 64, two times 16 lanes read and add in a fixed order.
 template <int D>
-__global__ void __launch_bounds__(256) packed_merge_kernel(const PackedArgs a) {
+__global__ void __launch_bounds__(kMergeThreads) packed_merge_kernel(const PackedArgs a) {
   grid_dependency_wait();
   if (a.head[2] == 0) return;
   constexpr int kLanes = D / 4, kRows = 32 / kLanes;   // lanes a partial row, rows at a time
+  constexpr unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31, sub = lane % kLanes, slot = lane / kLanes;
-  const int64_t at = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  if (at >= static_cast<int64_t>(a.N) * a.Hq) return;
-  const int n = a.row_splits[at / a.Hq];
-  if (n <= 1) return;
   const int64_t rows = static_cast<int64_t>(a.N) * a.Hq;
-  const float own = a.lse_own != nullptr ? a.lse_own[at] * kLog2e : -INFINITY;
-  float M = own;
-  for (int s = lane; s < n; s += 32) M = fmaxf(M, a.part_ml[2 * (s * rows + at)]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float base = M == -INFINITY ? 0.f : M;
-  float L = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = 0; c < n; c += 32) {
-    float f = 0.f;
-    if (c + lane < n) {
-      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * ((c + lane) * rows + at));
-      f = ex2(ml.x - base);
-      L += ml.y * f;
-    }
-    const int here = min(32, n - c);
-    const float* from = a.part_o + ((c + slot) * rows + at) * D + sub * 4;
-    int j0 = 0;
-    for (; j0 + 8 * kRows <= here; j0 += 8 * kRows) {
-      float4 v[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-        v[u] = *reinterpret_cast<const float4*>(from + (j0 + u * kRows) * rows * D);
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kMergeThreads / 32);
+  for (int64_t at = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5); at < rows; at += warps) {
+    const int n = a.row_splits[at / a.Hq];
+    if (n <= 1) continue;
+    const float* from = a.part_o + at * D + sub * 4;
+    float4 v[8];
+    auto load = [&](int j0) {
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const float fj = __shfl_sync(0xffffffffu, f, j0 + u * kRows + slot);
-        o.x = fmaf(v[u].x, fj, o.x);
-        o.y = fmaf(v[u].y, fj, o.y);
-        o.z = fmaf(v[u].z, fj, o.z);
-        o.w = fmaf(v[u].w, fj, o.w);
+        const int j = j0 + u * kRows + slot;
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j < n) v[u] = *reinterpret_cast<const float4*>(from + j * rows * D);
       }
-    }
-#pragma unroll 4
-    for (; j0 < here; j0 += kRows) {
-      const int j = j0 + slot;                   // at d = 64 the last may be one too many
-      float fj = __shfl_sync(0xffffffffu, f, min(j, 31));
-      if (j < here) {
-        const float4 v = *reinterpret_cast<const float4*>(from + j0 * rows * D);
-        o.x = fmaf(v.x, fj, o.x);
-        o.y = fmaf(v.y, fj, o.y);
-        o.z = fmaf(v.z, fj, o.z);
-        o.w = fmaf(v.w, fj, o.w);
-      }
-    }
-  }
+    };
+    load(0);
+    float2 x[2];
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-  if constexpr (kRows == 2) {
-    o.x += __shfl_xor_sync(0xffffffffu, o.x, 16);
-    o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
-    o.z += __shfl_xor_sync(0xffffffffu, o.z, 16);
-    o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
+    for (int i = 0; i < 2; ++i) {
+      x[i] = make_float2(-INFINITY, 0.f);
+      if (lane + 32 * i < n)
+        x[i] = *reinterpret_cast<const float2*>(a.part_ml + 2 * ((lane + 32 * i) * rows + at));
+    }
+    float own = -INFINITY;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a.lse_own != nullptr) {
+      own = a.lse_own[at] * kLog2e;
+      y = *reinterpret_cast<const float4*>(a.o_own + at * D + sub * 4);
+    }
+    float M = fmaxf(own, fmaxf(x[0].x, x[1].x));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
+    const float base = M == -INFINITY ? 0.f : M;
+    const float f0 = ex2(x[0].x - base), f1 = ex2(x[1].x - base);
+    float L = x[0].y * f0 + x[1].y * f1;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(kAll, L, o);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = 0; j0 < n; j0 += 8 * kRows) {
+      if (j0 > 0) load(j0);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int j = j0 + u * kRows + slot;      // a batch is in one half of the 64
+        const float f = __shfl_sync(kAll, j0 < 32 ? f0 : f1, j & 31);
+        o.x = fmaf(v[u].x, f, o.x);
+        o.y = fmaf(v[u].y, f, o.y);
+        o.z = fmaf(v[u].z, f, o.z);
+        o.w = fmaf(v[u].w, f, o.w);
+      }
+    }
+    if constexpr (kRows == 2) {
+      o.x += __shfl_xor_sync(kAll, o.x, 16);
+      o.y += __shfl_xor_sync(kAll, o.y, 16);
+      o.z += __shfl_xor_sync(kAll, o.z, 16);
+      o.w += __shfl_xor_sync(kAll, o.w, 16);
+    }
+    if (own != -INFINITY) {     // o_own is normalised: a part with l = 1 at its log-sum
+      const float f = ex2(own - base);
+      L += f;
+      o.x = fmaf(y.x, f, o.x);
+      o.y = fmaf(y.y, f, o.y);
+      o.z = fmaf(y.z, f, o.z);
+      o.w = fmaf(y.w, f, o.w);
+    }
+    const float inv = L == 0.f ? 0.f : 1.0f / L;
+    o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    __syncwarp();               // o_f32 may be o_own, lse lse_own: every lane has read them
+    if (slot == 0) {
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + at * D + sub * 4) =
+          make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+      if (a.o_f32 != nullptr) *reinterpret_cast<float4*>(a.o_f32 + at * D + sub * 4) = o;
+    }
+    if (lane == 0) a.lse[at] = L == 0.f ? -INFINITY : (base + log2f(L)) * kLn2;
   }
-  if (own != -INFINITY) {     // o_own is normalised: a part with l = 1 at its log-sum
-    const float f = ex2(own - base);
-    L += f;
-    const float4 v = *reinterpret_cast<const float4*>(a.o_own + at * D + sub * 4);
-    o.x = fmaf(v.x, f, o.x);
-    o.y = fmaf(v.y, f, o.y);
-    o.z = fmaf(v.z, f, o.z);
-    o.w = fmaf(v.w, f, o.w);
-  }
-  const float inv = L == 0.f ? 0.f : 1.0f / L;
-  o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-  __syncwarp();               // o_f32 may be o_own: every lane has read it
-  if (slot == 0) {
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + at * D + sub * 4) =
-        make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
-    if (a.o_f32 != nullptr) *reinterpret_cast<float4*>(a.o_f32 + at * D + sub * 4) = o;
-  }
-  if (lane == 0) a.lse[at] = L == 0.f ? -INFINITY : (base + log2f(L)) * kLn2;
 }
 
 template <int D>
@@ -1295,8 +1311,11 @@ cudaError_t launch_d(const PackedArgs& a, const CUtensorMap& tq, const CUtensorM
   const int grid = static_cast<int>(units < num_sms ? units : num_sms);
   e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s, a, tq, tk, tv);
   if (e != cudaSuccess || a.smax == 1) return e;
-  const int64_t warps = static_cast<int64_t>(a.N) * a.Hq;
-  return launch_pdl(packed_merge_kernel<D>, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0, s, a);
+  constexpr int kWarps = kMergeThreads / 32;
+  const int64_t blocks = (static_cast<int64_t>(a.N) * a.Hq + kWarps - 1) / kWarps;
+  const int64_t most = static_cast<int64_t>(kMergeBlocks) * num_sms;
+  return launch_pdl(packed_merge_kernel<D>, dim3(static_cast<unsigned>(std::min(blocks, most))),
+                    dim3(kMergeThreads), 0, s, a);
 }
 
 }  // namespace
