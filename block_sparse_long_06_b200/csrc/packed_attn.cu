@@ -54,7 +54,7 @@ constexpr int kRegsSoftmax = 192, kRegsOther = 56, kRegsOut = 72;
 static_assert(2 * kRegsSoftmax + kRegsOther + kRegsOut <= 65536 / 128, "registers of the launch");
 constexpr uint32_t kTmemCols = 512;
 constexpr int kStep = 128;             // keys a step
-constexpr int kMaxStages = 10;
+constexpr int kMaxStages = 11;
 constexpr int kRounds = 2;              // units a block may have where it plans for itself
 constexpr int kPlanThreads = 1024;
 constexpr int kMergeThreads = 256, kMergeBlocks = 4;    // blocks an SM
@@ -69,6 +69,9 @@ struct Cfg {
   static constexpr int kHalves = D / 64;            // 64-dim slabs (rows of 128 B)
   static constexpr int kSlab = 128 * 128;           // 128 rows of one slab
   static constexpr int kTile = kHalves * kSlab;     // 128 rows x D: a Q tile, or K or V of a step
+  // One more where no unit has two tiles: it takes the place of the second Q tile, before the
+  // others. A pair of steps of one tile uses four stages, so that with five the next keys come
+  // late: 2,250 cycles a step at d = 128 (keys in L2), 1,650 with six; from HBM 2,970 and 2,760.
   static constexpr int kStages = D == 128 ? 5 : 10;
   static constexpr int kOffKV = 2 * kTile;
   static constexpr int kOffBar = kOffKV + kStages * kTile;
@@ -76,6 +79,7 @@ struct Cfg {
 
 struct Unit {
   int u, b, g, row0, ntok, pos0, len, step0, step1, split, nsplit, bad;
+  int more;                            // stages besides kStages, the same for all units
 };
 
 struct Bars {
@@ -176,7 +180,7 @@ BSA_DEVFN int seq_len(const PackedArgs& a, int b) {
 }
 
 // What a step of a unit costs: with two tiles of rows it takes 3,010 cycles (d = 64: 2,820), with
-// one 2,290, which its keys take to arrive, and 1,460 at d = 64.
+// one 2,250 to 2,970, which its keys take to arrive, and 1,460 at d = 64.
 BSA_DEVFN int step_cost(int d, bool two) { return two ? 4 : d == 128 ? 3 : 2; }
 
 // Without splits the SMs are evenly loaded where there are several units for each SM and the
@@ -211,7 +215,7 @@ BSA_DEVFN float plan_time(const PackedArgs& a, float share, int units, int piece
 // One block: lists the units (tile, split of its keys) of one kv head, longest first.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) {
   __shared__ int warp_sum[32];
-  __shared__ int carry, bad, longest;
+  __shared__ int carry, bad, longest, wide;
   __shared__ unsigned long long work, best;   // best: (time, candidate)
   __shared__ int bucket[kBuckets], costs[kPlanTiles];
   // first row, length and first tile of each sequence, for up to kPlanSeqs of them
@@ -225,6 +229,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) 
     carry = 0;
     bad = 0;
     longest = 0;
+    wide = 0;
     work = 0;
     best = ~0ull;
   }
@@ -300,6 +305,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) 
   for (int t = tid; t < ntiles; t += kPlanThreads) {
     const int c = cost_of(tile(t));
     if (t < kPlanTiles) costs[t] = min(c, 0xfffff) | (tile(t).ntok << 20);
+    if (tile(t).ntok > half) wide = 1;
     sum += c;
     top = max(top, c);
   }
@@ -359,6 +365,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) 
     a.head[0] = before + x;
     a.head[1] = 0;
     a.head[2] = any ? 1 : 0;
+    a.head[3] = wide ? 0 : 1;
   }
   __syncthreads();
   for (int t = tid; t < ntiles; t += kPlanThreads) {
@@ -394,7 +401,7 @@ BSA_DEVFN int unit_of_round(int k) {
 // 48 instead of 55, 693 rows over 3K keys (16/8 heads, d = 64) 43 and 47; where units that blocks
 // take when they are free would be better it loses (27 rows each of 16 sequences over 12K keys,
 // 64/4 heads: 122 and 114). Four rounds: 200 rows behind three prefixes 483 us, 378 with two.
-BSA_DEVFN int plan_in_warp(const PackedArgs& a, int4* own) {
+BSA_DEVFN int plan_in_warp(const PackedArgs& a, int4* own, int& more) {
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31;
   const int per = packed_unit_tokens(a.G), half = per / 2;
@@ -466,6 +473,7 @@ BSA_DEVFN int plan_in_warp(const PackedArgs& a, int4* own) {
     entries += m;
   }
   const bool any = __any_sync(kAll, n > 1);
+  more = __any_sync(kAll, x.ntok > half) ? 0 : 1;
   if (first_block) {
     if (any)
       for (int r = end + lane; r < a.N; r += 32) a.row_splits[r] = 0;
@@ -676,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->o_full[x], 1);
     }
     mbar_init(&bars->mma_done, 1);
-    for (int s = 0; s < NS; ++s) {
+    for (int s = 0; s < NS + 1; ++s) {
       mbar_init(&bars->kv_full[s], 1);
       mbar_init(&bars->kv_empty[s], 1);
       mbar_init(&bars->kv_raw[s], 1);
@@ -699,8 +707,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   grid_launch_dependents();            // the merge kernel may be set up, and waits for this one
   grid_dependency_wait();
-  int own_units = 0;                   // (before the registers are shared out: it takes more)
-  if (a.in_block && warp == kWarpLoad) own_units = plan_in_warp(a, bars->own);
+  int own_units = 0, more = 0;         // (before the registers are shared out: it takes more)
+  if (a.in_block && warp == kWarpLoad) own_units = plan_in_warp(a, bars->own, more);
 
   if (warp >= kWarpOut) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRegsOut));
@@ -709,12 +717,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRegsOther));
     if (warp == kWarpLoad) {
       // ------------------------------------------------------------------ units, K, V
-      uint32_t un = 0, kc = 0;
+      uint32_t un = 0, st = 0, phase = 1;      // the next stage of the ring
       bool ok = true;
       int next = 0, units = 0;
       while (ok) {
         const int slot = un & 1;
-        Unit U = {-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+        Unit U = {-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
         // the first unit; the others come from the counter
         int u = blockIdx.x;
         if (un > 0) u = a.in_block ? unit_of_round(un)
@@ -728,7 +736,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         int e = min(u / a.Hkv, a.max_entries - 1), g = u % a.Hkv;
         const int4* from = a.in_block ? bars->own + 2 * (un % kRounds) : a.entries + 2 * e;
         int4 e0 = from[0], e1 = from[1];
-        if (un == 0) units = a.in_block ? own_units : a.head[0] * a.Hkv;
+        if (un == 0) {
+          units = a.in_block ? own_units : a.head[0] * a.Hkv;
+          if (!a.in_block) more = a.head[3];
+        }
         if (un == kRounds && a.in_block) units = 0;
         if (!a.causal && units > static_cast<int>(gridDim.x) && u < units) {
           g = u / (units / a.Hkv);
@@ -769,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return bad;
         };
         if (u < units) {
-          U = {u, e0.x, g, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w & 0xffff, e1.w >> 16, 0};
+          U = {u, e0.x, g, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w & 0xffff, e1.w >> 16, 0, more};
           nblk = (U.len + kBlock - 1) / kBlock;
           // blocks with a bad page or beyond the cache are found before the unit starts
           bool bad = look_up(2 * U.step0);
@@ -807,18 +818,21 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (s0 + q == max(U.step1 - 3, U.step0) && !a.in_block) next = atomicAdd(&a.head[1], 1);
               // a step that has the sequence's end or a bad block goes through the patch warp
               const bool patch = (s0 + q + 1) * kStep > U.len || k0 < 0 || k1 < 0;
-              for (int kv = 0; kv < 2 && ok; ++kv, ++kc) {
-                const int s = kc % NS;
-                if (!mbar_wait_sleep(&bars->kv_empty[s], ((kc / NS) & 1) ^ 1)) { ok = false; break; }
-                uint64_t* bar = kv == 1 && patch ? &bars->kv_raw[s] : &bars->kv_full[s];
+              for (int kv = 0; kv < 2 && ok; ++kv) {
+                if (!mbar_wait_sleep(&bars->kv_empty[st], phase)) { ok = false; break; }
+                uint64_t* bar = kv == 1 && patch ? &bars->kv_raw[st] : &bars->kv_full[st];
                 const int r0 = kv ? v0 : k0, r1 = kv ? v1 : k1;
                 const uint32_t bytes = ((r0 >= 0) + (r1 >= 0)) * (C::kTile / 2);
                 if (bytes > 0) mbar_arrive_expect_tx(bar, bytes); else mbar_arrive(bar);
-                unsigned char* st = smem + C::kOffKV + s * C::kTile;
+                unsigned char* to = smem + C::kOffKV + (static_cast<int>(st) - more) * C::kTile;
                 const CUtensorMap* map = kv ? &tmv : &tmk;
                 for (int x = 0; x < C::kHalves; ++x) {
-                  if (r0 >= 0) tma_load_2d(st + x * C::kSlab, map, x * 64, r0, bar);
-                  if (r1 >= 0) tma_load_2d(st + x * C::kSlab + 8192, map, x * 64, r1, bar);
+                  if (r0 >= 0) tma_load_2d(to + x * C::kSlab, map, x * 64, r0, bar);
+                  if (r1 >= 0) tma_load_2d(to + x * C::kSlab + 8192, map, x * 64, r1, bar);
+                }
+                if (++st == NS + more) {
+                  st = 0;
+                  phase ^= 1;
                 }
               }
             }
@@ -828,9 +842,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (lane == 0 && !ok) {
         set_abort(bars, a.status);
-        // copies in flight must land before the block exits (bounded)
-        for (uint32_t k = (kc > NS ? kc - NS : 0); k < kc; ++k)
-          mbar_wait_sleep(&bars->kv_full[k % NS], (k / NS) & 1, 100000000ull);
+        // copies in flight must land before the block exits (bounded): the last of each stage
+        for (uint32_t k = 0; k < static_cast<uint32_t>(NS + more); ++k)
+          mbar_wait_sleep(&bars->kv_full[k], k < st ? phase ^ 1 : phase, 100000000ull);
       }
     } else if (warp == kWarpQ && lane == 0) {
       // ------------------------------------------------------------------------------ Q
@@ -896,10 +910,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (!patch) continue;
-          const int s = (kc + 2 * j + 1) % NS;
+          const int s = (kc + 2 * j + 1) % (NS + U.more);
           if (!warp_wait_sleep(&bars->kv_raw[s], (raw_phase >> s) & 1)) { ok = false; break; }
           raw_phase ^= 1u << s;
-          unsigned char* st = smem + C::kOffKV + s * C::kTile;
+          unsigned char* st = smem + C::kOffKV + (s - U.more) * C::kTile;
           for (int x = 0; x < C::kHalves; ++x)
             for (int i = 0; i < 2; ++i)
               for (int c = keep[i] * 8 + lane; c < kBlock * 8; c += 32)
@@ -933,10 +947,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         int st;
         uint32_t phase;
       };
-      auto step = [](Pos& p) {                     // to the same operand of the next step
+      int more = 0;
+      auto step = [&](Pos& p) {                    // to the same operand of the next step
         p.st += 2;
-        if (p.st >= NS) {
-          p.st -= NS;
+        if (p.st >= NS + more) {
+          p.st -= NS + more;
           p.phase ^= 1;
         }
       };
@@ -953,6 +968,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++un;
           const bool stop = U.u < 0 || aborted(bars);
           one = U.ntok <= half_tok;
+          more = U.more;
           total = stop ? 0 : (U.step1 - U.step0) * (one ? 1 : 2);
           if (stop || total > 0) return true;
         }
@@ -963,7 +979,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto release = [&](const Pos& p) { tc::commit(&bars->kv_empty[p.st]); };
       // S of tile t from Q tile q
       auto scores = [&](int t, int q, const Pos& p) {
-        uint64_t dq = dq0 + ((q * C::kTile) >> 4), dk = dk0 + ((p.st * C::kTile) >> 4);
+        uint64_t dq = dq0 + ((q * C::kTile) >> 4), dk = dk0 + (((p.st - more) * C::kTile) >> 4);
         keep(dq);
         keep(dk);
         tc::fence_after_sync();
@@ -979,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t s_tm = tmem + 256 + 128 * t, o_tm = tmem + 128 * t;
         const uint32_t phase = (p_phase >> t) & 1;
         p_phase ^= 1u << t;
-        uint64_t dv = dv0 + ((p.st * C::kTile) >> 4);
+        uint64_t dv = dv0 + (((p.st - more) * C::kTile) >> 4);
         keep(dv);
         if (first && !mbar_wait(&bars->o_empty[t], o_phase)) return false;
         if (!mbar_wait(&bars->p_ready[t][0], phase) || !full(p)) return false;

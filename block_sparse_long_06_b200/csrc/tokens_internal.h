@@ -41,7 +41,7 @@ struct PackedArgs {
   float* lse;                 // [N, Hq]
   float* o_f32;               // [N, Hq, d] or null
   int32_t* status;
-  int32_t* head;              // plan: [0] entries, [1] unit counter, [2] any row split
+  int32_t* head;              // plan: [0] entries, [1] unit counter, [2] any row split, [3] no unit has two tiles
   int32_t* offs;              // plan: [B+1] first tile of each sequence
   int4* entries;              // plan: two int4 an entry
   int32_t* row_splits;        // plan: [N] partial results of each row (0: row not written)
