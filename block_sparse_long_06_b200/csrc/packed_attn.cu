@@ -194,21 +194,26 @@ BSA_DEVFN int step_cost(int d, bool two) { return two ? 4 : d == 128 ? 3 : 2; }
 BSA_DEVFN int candidate(int i, float share) {
   return i == 0 ? 1 << 30 : max(12, static_cast<int>(share * (0.1f + 0.06f * i)) + 1);
 }
+// Pieces that a tile of cost c is cut into where a piece may cost 1 / per, and what one costs. In
+// floats, which are a few instructions each: a block that plans for itself waits for its plan.
+BSA_DEVFN int pieces(const PackedArgs& a, int c, float per) {
+  return max(1, min(a.smax, __float2int_ru(c * per - 0.001f)));
+}
+BSA_DEVFN int piece_cost(int c, int k) { return __float2int_ru(__fdividef(c, k) - 0.001f); }
 // What a tile of cost c and ntok tokens adds under the candidate: units and the rows (of one kv
 // head) that go through the merge; the costliest piece.
-BSA_DEVFN void add_tile(const PackedArgs& a, int c, int ntok, int cand, int& units, int& piece, int& parts) {
-  const int k = max(1, min(a.smax, (c + cand - 1) / cand));
+BSA_DEVFN void add_tile(const PackedArgs& a, int c, int ntok, float per, int& units, int& piece, int& parts) {
+  const int k = pieces(a, c, per);
   units += k;
-  piece = max(piece, (c + k - 1) / k);
+  piece = max(piece, piece_cost(c, k));
   if (k > 1) parts += k * ntok * a.G;
 }
 BSA_DEVFN float plan_time(const PackedArgs& a, float share, int units, int piece, int parts) {
-  const float unit = piece + kUnitCost;
-  const float merge = (parts > 0 ? kMergeCost : 0.f) +
-                      static_cast<float>(parts) * a.Hkv / (kRowsCost * a.num_sms);
+  const float unit = piece + kUnitCost, sms = a.num_sms, per_sm = __fdividef(1.f, sms);
+  const float merge = (parts > 0 ? kMergeCost : 0.f) + parts * a.Hkv * per_sm * (1.f / kRowsCost);
   // an SM's share of all costs; its share of the units in whole rounds
-  const float even = share + units * kUnitCost / a.num_sms;
-  const float rounds = even * a.num_sms / max(units, 1) * ((units + a.num_sms - 1) / a.num_sms);
+  const float even = share + units * kUnitCost * per_sm;
+  const float rounds = __fdividef(even * sms, max(units, 1)) * ceilf(units * per_sm - 0.001f);
   return merge + (units <= a.num_sms ? unit : max(rounds, even + 0.2f * unit));
 }
 
@@ -322,9 +327,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) 
   if (a.smax > 1 && ntiles <= kPlanTiles &&
       !(static_cast<float>(longest) <= share && static_cast<long long>(ntiles) * a.Hkv >= 3ll * a.num_sms)) {
     const int cand = candidate(warp, share);    // a warp for each
+    const float per_cost = __fdividef(1.f, cand);
     int units = 0, piece = 0, parts = 0;
     for (int t = lane; t < ntiles; t += 32)
-      add_tile(a, costs[t] & 0xfffff, costs[t] >> 20, cand, units, piece, parts);
+      add_tile(a, costs[t] & 0xfffff, costs[t] >> 20, per_cost, units, piece, parts);
     units = __reduce_add_sync(0xffffffffu, units) * a.Hkv;
     parts = __reduce_add_sync(0xffffffffu, parts);
     piece = __reduce_max_sync(0xffffffffu, piece);
@@ -334,9 +340,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedArgs a) 
     __syncthreads();
     limit = static_cast<int>(best & 0x7fffffffull);
   }
+  const float per_limit = __fdividef(1.f, limit);
   const int shift = max(0, 32 - __clz(longest) - 9);
   auto splits_of = [&](const Tile& x) {
-    return max(1, min(min(a.smax, x.steps), (cost_of(x) + limit - 1) / limit));
+    return max(1, min(x.steps, pieces(a, cost_of(x), per_limit)));
   };
   auto bucket_of = [&](const Tile& x, int n) {
     return kBuckets - 1 - min(kBuckets - 1, ((cost_of(x) + n - 1) / n) >> shift);
@@ -453,24 +460,30 @@ BSA_DEVFN int plan_in_warp(const PackedArgs& a, int4* own, int& more) {
     }
   }
   if (a.smax > 1) {
-    const float share = static_cast<float>(__reduce_add_sync(kAll, c)) * a.Hkv / a.num_sms;
-    const int cand = candidate(lane, share);
+    const float share = static_cast<float>(__reduce_add_sync(kAll, static_cast<unsigned>(c))) * a.Hkv / a.num_sms;
+    const float cand = __fdividef(1.f, candidate(lane, share));
     int units = 0, piece = 0, parts = 0;
+#pragma unroll 1
     for (int t = 0; t < ntiles; ++t)
       add_tile(a, __shfl_sync(kAll, c, t), __shfl_sync(kAll, x.ntok, t), cand, units, piece, parts);
     units *= a.Hkv;
     const float time = units <= kRounds * a.num_sms ? plan_time(a, share, units, piece, parts) : INFINITY;
     const unsigned best = __reduce_min_sync(kAll, __float_as_uint(time));
-    const int limit = __shfl_sync(kAll, cand, __ffs(__ballot_sync(kAll, __float_as_uint(time) == best)) - 1);
-    if (lane < ntiles) n = max(1, min(min(a.smax, x.steps), (c + limit - 1) / limit));
+    const float limit = __shfl_sync(kAll, cand, __ffs(__ballot_sync(kAll, __float_as_uint(time) == best)) - 1);
+    if (lane < ntiles) n = max(1, min(x.steps, pieces(a, c, limit)));
   }
-  // units of costlier pieces, and of equal ones before this one, come first
-  const int piece = n > 0 ? (c + n - 1) / n : -1;
-  int at = 0, entries = 0;
-  for (int t = 0; t < ntiles; ++t) {
-    const int p = __shfl_sync(kAll, piece, t), m = __shfl_sync(kAll, n, t);
-    if (p > piece || (p == piece && t < lane)) at += m;
-    entries += m;
+  // units of costlier pieces, and of equal ones before this one, come first; without splits all
+  // units run at once, and their order is nothing
+  int at = lane, entries = ntiles;
+  if (a.smax > 1) {
+    const int piece = n > 0 ? piece_cost(c, n) : -1;
+    at = entries = 0;
+#pragma unroll 1
+    for (int t = 0; t < ntiles; ++t) {
+      const int p = __shfl_sync(kAll, piece, t), m = __shfl_sync(kAll, n, t);
+      if (p > piece || (p == piece && t < lane)) at += m;
+      entries += m;
+    }
   }
   const bool any = __any_sync(kAll, n > 1);
   more = __any_sync(kAll, x.ntok > half) ? 0 : 1;
@@ -480,6 +493,7 @@ BSA_DEVFN int plan_in_warp(const PackedArgs& a, int4* own, int& more) {
     if (lane == 0) a.head[2] = any ? 1 : 0;
   }
   const int units = entries * a.Hkv;
+#pragma unroll 1
   for (int k = 0; k < kRounds; ++k) {
     const int u = unit_of_round(k);
     if (u >= units) break;
