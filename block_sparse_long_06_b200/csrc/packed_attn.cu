@@ -632,7 +632,7 @@ BSA_DEVFN void out_role(const PackedArgs& a, Bars* bars, uint32_t tmem) {
             if (one) mbar_arrive(&bars->o_empty[1]);
           }
         }
-        if (live && own != 0.f) {
+        if (w != -INFINITY) {                  // (then live; the weight itself may be NaN)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float4 y = *reinterpret_cast<const float4*>(a.o_own + at * D + c + 4 * i);

@@ -602,3 +602,36 @@ def test_the_own_part_is_joined_once(rows, lens):
     own[1][0, :2], own[1][cu[1], :] = 200.0, -math.inf
     step = run_shared(q, mem, cu, lens, Hkv, own)
     check(step, exact_shared(q, mem, cu, lens, G, own), max(lens), d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", [[1, 20, 3], [90, 2, 33]])
+def test_what_other_rows_hold_has_no_effect(d, rows):
+    """Padding rows and other sequences' rows share tiles with a sequence's: NaN or infinite
+    there, its bits stay."""
+    G, Hkv = 8, 2
+    lens = [1700, 300, 129]
+    cu = sums(rows)
+    mem = Paged(lens, Hkv, d, seed=100)
+    q = randn(cu[-1] + 40, Hkv * G, d, seed=101, scale=1.5)
+    want = run_attend(q, mem, cu, lens, Hkv)
+    bad = q.clone()
+    bad[cu[1]:] = float("nan")
+    bad[cu[1] + 1::2] = float("inf")
+    got = run_attend(bad, mem, cu, lens, Hkv)
+    for a, b in ((got.o, want.o), (got.lse, want.lse), (got.o_f32, want.o_f32)):
+        assert torch.equal(a[:cu[1]], b[:cu[1]])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_units_of_odd_numbers_of_steps(d):
+    """A block's units with one tile of rows and with two, of one step and of many, one after the
+    other: buffers of scores and stages go on where the last unit left them."""
+    G, Hkv = 4, 1
+    new = [1, 64, 1, 33, 2, 70, 1, 5, 64, 1, 1, 40] * 40
+    lens = [n + (b * 97) % 700 for b, n in enumerate(new)]
+    cu = sums(new)
+    mem = Paged(lens, Hkv, d, seed=102)
+    q = randn(cu[-1], Hkv * G, d, seed=103, scale=1.5)
+    step = run_attend(q, mem, cu, lens, Hkv)
+    check(step, exact(q, mem, cu, lens, True, G), max(lens), d)
