@@ -33,7 +33,7 @@
 //  * Rows of V behind a sequence's end are whatever the page held before: a patch warp
 //    zeroes them in shared memory in the step that has the end (0 * NaN is NaN), before the
 //    step is handed to the tensor cores. K there may be anything: its scores are replaced.
-// Tensor memory: O of tile t at 128 t, S (and P) of tile t at 256 + 128 t. Every wait is
+// Tensor memory: O of tile t at d t, the scores' buffers (then P) of 128 columns from 2 d. Every wait is
 // bounded; on a timeout the kernel reports BSA_DEV_TIMEOUT, drains and returns.
 #include <algorithm>
 
@@ -47,8 +47,7 @@ namespace {
 constexpr int kThreads = 512;          // warps 0-3 / 4-7: softmax of tile 0 / 1; then one each:
 constexpr int kSoftmaxWarps = 8, kWarpLoad = 8, kWarpMma = 9, kWarpPatch = 10, kWarpQ = 11;
 constexpr int kWarpOut = 12;           // and 12-15: results
-// of every kPolyOf pairs of a row's scores, kPoly take their exponentials by polynomial
-constexpr int kPolyOf = 8, kPoly = 1;
+constexpr int kPolyOf = 8;             // see Cfg
 // registers a thread of the softmax warps, of the warps 8-11 and of 12-15
 constexpr int kRegsSoftmax = 192, kRegsOther = 56, kRegsOut = 72;
 static_assert(2 * kRegsSoftmax + kRegsOther + kRegsOut <= 65536 / 128, "registers of the launch");
@@ -73,6 +72,13 @@ struct Cfg {
   // others. A pair of steps of one tile uses four stages, so that with five the next keys come
   // late: 2,250 cycles a step at d = 128 (keys in L2), 1,650 with six; from HBM 2,970 and 2,760.
   static constexpr int kStages = D == 128 ? 5 : 10;
+  // Of every kPolyOf pairs of a row's scores, kPoly take their exponentials by polynomial. At
+  // d = 128 more cost power, which is the limit there; at d = 64 a step of two tiles takes 2,650
+  // cycles with none, 2,730 with 1, 2,610 with 2 and 3,150 with 3.
+  static constexpr int kPoly = D == 128 ? 1 : 2;
+  // Buffers of scores: one a tile, or three that the tiles take in turn (see the issuer).
+  static constexpr int kRing = D == 128 ? 2 : 3;
+  static constexpr int kScores = 2 * D;             // their first column in tensor memory
   static constexpr int kOffKV = 2 * kTile;
   static constexpr int kOffBar = kOffKV + kStages * kTile;
 };
@@ -86,8 +92,9 @@ struct Bars {
   uint64_t info_full[2], info_empty[2];
   uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], kv_raw[kMaxStages];
-  uint64_t s_full[2], o_full[2];
-  uint64_t p_ready[2][2];              // [tile][half of the step's keys]
+  uint64_t s_full[2][3];               // [tile][buffer]
+  uint64_t pv_done[2], o_full[2];      // pv_done: with three buffers
+  uint64_t p_ready[3][2];              // [buffer][half of the step's keys]
   uint64_t ml_full[2], o_empty[2];     // a unit's (m, l) is written; its O and (m, l) are read
   uint64_t mma_done;
   float2 ml[2][128];                   // [tile][row]
@@ -603,7 +610,7 @@ BSA_DEVFN void out_role(const PackedArgs& a, Bars* bars, uint32_t tmem) {
         else
           a.lse[at] = L == 0.f ? -INFINITY : (m + log2f(L)) * kLn2;
       }
-      const uint32_t o_tm = tmem + lane_addr + 128 * t;
+      const uint32_t o_tm = tmem + lane_addr + D * t;
 #pragma unroll 1
       for (int c = 0; c < D; c += 16) {
         __syncwarp();
@@ -618,7 +625,7 @@ BSA_DEVFN void out_role(const PackedArgs& a, Bars* bars, uint32_t tmem) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(x[i]) * f0;
           if (two) {
-            ld16(o_tm + 128 + c, x);
+            ld16(o_tm + D + c, x);
             tc::wait_ld();
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = fmaf(__uint_as_float(x[i]), f1, v[i]);
@@ -690,9 +697,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->info_empty[x], 7 + kSoftmaxWarps);   // with the issuer, patch, Q, out warps
       mbar_init(&bars->q_full[x], 1);
       mbar_init(&bars->q_empty[x], 1);
-      mbar_init(&bars->s_full[x], 1);
-      mbar_init(&bars->p_ready[x][0], 4);    // the tile's softmax warps
-      mbar_init(&bars->p_ready[x][1], 4);
+      for (int b = 0; b < 3; ++b) {
+        mbar_init(&bars->s_full[x][b], 1);
+        mbar_init(&bars->p_ready[b][x], 4);  // the tile's softmax warps
+      }
+      mbar_init(&bars->pv_done[x], 1);
       mbar_init(&bars->ml_full[x], 4);
       mbar_init(&bars->o_empty[x], 4);       // the out warps
       mbar_init(&bars->o_full[x], 1);
@@ -955,7 +964,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dq0 = tc::smem_desc_sw128(sbase, 16, 1024);
       const uint64_t dk0 = tc::smem_desc_sw128(sbase + C::kOffKV, 16, 1024);
       const uint64_t dv0 = tc::smem_desc_sw128(sbase + C::kOffKV, C::kSlab, 1024);
-      uint32_t un = 0, q_phase = 0, p_phase = 0;   // phases: a bit for each tile
+      uint32_t un = 0, q_phase = 0, p_phase = 0;   // phases: a bit for each tile or buffer
       uint32_t o_phase = 1;                        // of o_empty, at the unit before
       struct Pos {                                 // a stage of the ring and its phase
         int st;
@@ -991,8 +1000,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto keep = [](uint64_t& desc) { asm volatile("" : "+l"(desc)); };
       auto full = [&](const Pos& p) { return mbar_wait(&bars->kv_full[p.st], p.phase); };
       auto release = [&](const Pos& p) { tc::commit(&bars->kv_empty[p.st]); };
-      // S of tile t from Q tile q
-      auto scores = [&](int t, int q, const Pos& p) {
+      // S of tile t from Q tile q, in buffer b
+      auto scores = [&](int t, int b, int q, const Pos& p) {
         uint64_t dq = dq0 + ((q * C::kTile) >> 4), dk = dk0 + (((p.st - more) * C::kTile) >> 4);
         keep(dq);
         keep(dk);
@@ -1000,24 +1009,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t off = ((ks >> 2) * C::kSlab + (ks & 3) * 32) >> 4;
-          tc::mma_ss(tmem + 256 + 128 * t, dq + off, dk + off, idS, ks > 0);
+          tc::mma_ss(tmem + C::kScores + 128 * b, dq + off, dk + off, idS, ks > 0);
         }
-        tc::commit(&bars->s_full[t]);
+        tc::commit(&bars->s_full[t][C::kRing == 2 ? 0 : b]);
       };
-      // O of tile t += P V, P in two parts as the softmax hands them over
-      auto values = [&](int t, const Pos& p, bool first) {
-        const uint32_t s_tm = tmem + 256 + 128 * t, o_tm = tmem + 128 * t;
-        const uint32_t phase = (p_phase >> t) & 1;
-        p_phase ^= 1u << t;
+      // O of tile t += P V, P (buffer b) in two parts as the softmax hands them over
+      auto values = [&](int t, int b, const Pos& p, bool first) {
+        const uint32_t s_tm = tmem + C::kScores + 128 * b, o_tm = tmem + D * t;
+        const uint32_t phase = (p_phase >> b) & 1;
+        p_phase ^= 1u << b;
         uint64_t dv = dv0 + (((p.st - more) * C::kTile) >> 4);
         keep(dv);
         if (first && !mbar_wait(&bars->o_empty[t], o_phase)) return false;
-        if (!mbar_wait(&bars->p_ready[t][0], phase) || !full(p)) return false;
+        if (!mbar_wait(&bars->p_ready[b][0], phase) || !full(p)) return false;
         tc::fence_after_sync();
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           tc::mma_ts(o_tm, s_tm + kk * 8, dv + ((kk * 2048) >> 4), idPV, !first || kk > 0);
-        if (!mbar_wait(&bars->p_ready[t][1], phase)) return false;
+        if (!mbar_wait(&bars->p_ready[b][1], phase)) return false;
         tc::fence_after_sync();
 #pragma unroll
         for (int kk = 4; kk < 8; ++kk)
@@ -1030,50 +1039,90 @@ __global__ void __launch_bounds__(kThreads, 1)
         return mbar_wait(&bars->q_full[t], phase);
       };
       // Pair i is step i / 2 of tile i % 2 (the K and V of a step are used twice) or, with one
-      // tile of rows, step i in tile i % 2 of tensor memory.
+      // tile of rows, step i in tile i % 2 of tensor memory. With a buffer of scores for each
+      // tile, pair i + 2 is scored behind the P V of pair i: a tile's softmax waits for it,
+      // for a part of 2,820 cycles. At d = 64 tensor memory has room for a third, which the
+      // tiles take in turn, and pair i + 3 is scored then (2,730 cycles; 1,008 rows over 9K keys,
+      // 64/4 heads, 949 us instead of 1,012). There the softmax warps' issue slots are the limit.
+      int ring = 0;                                // with three: the buffer of the unit's pair 0
       bool ok = fetch();
       while (ok && total > 0) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int q = one ? 0 : t;
-          if (t >= total || !ok) break;
-          if (t == 0 || !one) ok = query(q);
-          ok = ok && full(kp);
-          if (!ok) break;
-          scores(t, q, kp);
-          // Q is free after the unit's last scores
-          if (one ? t + 1 == total : t + 2 >= total) tc::commit(&bars->q_empty[q]);
-          if (one || t == 1) {
-            release(kp);
-            step(kp);
-          }
-        }
-        for (int i0 = 0; i0 < total && ok; i0 += 2) {
+        if constexpr (C::kRing == 2) {
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            const int i = i0 + t, q = one ? 0 : t;
-            if (i >= total) break;
-            ok = values(t, vp, i0 == 0);
+            const int q = one ? 0 : t;
+            if (t >= total || !ok) break;
+            if (t == 0 || !one) ok = query(q);
+            ok = ok && full(kp);
             if (!ok) break;
-            const bool more = i + 2 < total;
-            if (more) {
-              if (one || t == 0) ok = full(kp);
-              if (!ok) break;
-              scores(t, q, kp);
-              if (one ? i + 3 == total : i + 4 >= total) tc::commit(&bars->q_empty[q]);
-            } else {
-              tc::commit(&bars->o_full[t]);
-            }
-            // the stages behind the scores: a commit takes its time, and the softmax waits for S
+            scores(t, t, q, kp);
+            // Q is free after the unit's last scores
+            if (one ? t + 1 == total : t + 2 >= total) tc::commit(&bars->q_empty[q]);
             if (one || t == 1) {
-              release(vp);
-              step(vp);
+              release(kp);
+              step(kp);
+            }
+          }
+          for (int i0 = 0; i0 < total && ok; i0 += 2) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int i = i0 + t, q = one ? 0 : t;
+              if (i >= total) break;
+              ok = values(t, t, vp, i0 == 0);
+              if (!ok) break;
+              const bool more = i + 2 < total;
               if (more) {
-                release(kp);
-                step(kp);
+                if (one || t == 0) ok = full(kp);
+                if (!ok) break;
+                scores(t, t, q, kp);
+                if (one ? i + 3 == total : i + 4 >= total) tc::commit(&bars->q_empty[q]);
+              } else {
+                tc::commit(&bars->o_full[t]);
+              }
+              // the stages behind the scores: a commit takes its time, and the softmax waits for S
+              if (one || t == 1) {
+                release(vp);
+                step(vp);
+                if (more) {
+                  release(kp);
+                  step(kp);
+                }
               }
             }
           }
+        } else {
+          int sb = ring, vb = ring;                // the next buffers of scores and of values
+          // pair i is scored; `after` of the unit come after it
+          auto score = [&](int i, int after) {
+            const int t = i & 1, q = one ? 0 : t;
+            if (i < 2 && (i == 0 || !one)) ok = query(q);
+            ok = ok && full(kp);
+            if (!ok) return;
+            scores(t, sb, q, kp);
+            if (++sb == C::kRing) sb = 0;
+            if (one ? after == 0 : after < 2) tc::commit(&bars->q_empty[q]);
+            if (one || t == 1) {
+              release(kp);
+              step(kp);
+            }
+          };
+#pragma unroll 1
+          for (int i = 0; i < C::kRing && i < total && ok; ++i) score(i, total - 1 - i);
+#pragma unroll 1
+          for (int i = 0; i < total && ok; ++i) {
+            const int t = i & 1;
+            ok = values(t, vb, vp, i < 2);
+            if (!ok) break;
+            tc::commit(&bars->pv_done[t]);
+            if (++vb == C::kRing) vb = 0;
+            if (i + C::kRing < total) score(i + C::kRing, total - 1 - i - C::kRing);
+            if (i + 2 >= total) tc::commit(&bars->o_full[t]);
+            if (one || t == 1) {
+              release(vp);
+              step(vp);
+            }
+          }
+          ring = vb;
         }
         o_phase ^= 1;
         if (ok) ok = fetch();
@@ -1091,9 +1140,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t s_col = tmem + lane_addr + 256 + 128 * t;
+    const uint32_t o_col = tmem + lane_addr + D * t;
+    uint32_t s_col = tmem + lane_addr + C::kScores + 128 * t;
+    uint32_t ring = 0, buf = t;                // with three buffers: of the unit's pair 0, of this step
     const float sc = a.scale_log2;
-    // barrier phases, a bit each: 0 o_empty, at the unit before, 3 s_full, 4-5 units mod 4
+    // barrier phases, a bit each: 0 o_empty, at the unit before, 3 s_full (with three buffers:
+    // pv_done), 4-5 units mod 4, 6-8 s_full of three buffers
     uint32_t bits = 1;
     while (true) {
       const int slot = (bits >> 4) & 1;
@@ -1104,7 +1156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Read again where it is needed and given back at the end: what lives across the step
       // loop takes registers from the scores.
       const volatile Unit& U = bars->info[slot];
-      bits = (bits & 15) | ((bits + 16) & 48);
+      bits = (bits & ~48u) | ((bits + 16) & 48);
       if (U.u < 0 || aborted(bars)) break;
       float m = -INFINITY;
       float2 l = make_float2(0.f, 0.f);
@@ -1124,11 +1176,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         idle = tok0 + ((quarter * 32) >> a.lgG) >= U.ntok;
       }
       for (; left > 0; left -= stride, lim -= stride * kStep, bits ^= 8) {
-        if (!warp_wait_all(&bars->s_full[t], (bits >> 3) & 1)) { ok = false; break; }
+        if constexpr (C::kRing == 2) {
+          if (!warp_wait_all(&bars->s_full[t][0], (bits >> 3) & 1)) { ok = false; break; }
+        } else {
+          if (!warp_wait_all(&bars->s_full[t][buf], (bits >> (6 + buf)) & 1)) { ok = false; break; }
+          bits ^= 64u << buf;
+          s_col = tmem + lane_addr + C::kScores + 128 * buf;
+        }
+        uint64_t* ready = bars->p_ready[buf];
+        if constexpr (C::kRing == 3) buf = buf == 0 ? 2 : buf - 1;     // two pairs on
         if (idle) {   // rows of P that nobody reads
           if (lane == 0) {
-            mbar_arrive(&bars->p_ready[t][0]);
-            mbar_arrive(&bars->p_ready[t][1]);
+            mbar_arrive(&ready[0]);
+            mbar_arrive(&ready[1]);
           }
           continue;
         }
@@ -1176,15 +1236,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = x;
           }
           if (left < U.step1 - U.step0 - (stride - 1) * t) {
-            // the tile's P V of the last step is done (its S was issued behind it)
+            // the tile's P V of the last step is done: with two buffers its S was issued behind it
+            if constexpr (C::kRing == 3) {
+              if (!warp_wait_all(&bars->pv_done[t], ((bits >> 3) & 1) ^ 1)) { ok = false; break; }
+              tc::fence_after_sync();
+            }
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               uint32_t ov[32];
-              tc::ld32(s_col - 256 + c, ov);   // O of the tile
+              tc::ld32(o_col + c, ov);
               tc::wait_ld();
 #pragma unroll
               for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f);
-              tc::st32(s_col - 256 + c, ov);
+              tc::st32(o_col + c, ov);
             }
           }
         }
@@ -1198,7 +1262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 32; c += 2) {
               const float2 v = __ffma2_rn(
                   make_float2(__uint_as_float(s[i][c]), __uint_as_float(s[i][c + 1])), sc2, neg2);
-              const float2 p = (c / 2) % kPolyOf >= kPolyOf - kPoly
+              const float2 p = (c / 2) % kPolyOf >= kPolyOf - C::kPoly
                                    ? exp2_poly(v) : make_float2(ex2(v.x), ex2(v.y));
               l = __fadd2_rn(l, p);
               s[i >> 1][(i & 1) * 16 + c / 2] = pack_bf16(p.x, p.y);
@@ -1208,7 +1272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::wait_st();
           tc::fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->p_ready[t][h]);
+          if (lane == 0) mbar_arrive(&ready[h]);
         }
       }
       if (!ok || aborted(bars)) {
@@ -1222,6 +1286,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         bits ^= 1;
+        if constexpr (C::kRing == 3) {
+          const int n = U.step1 - U.step0;
+          ring = (ring + (U.ntok <= half_tok ? n : 2 * n)) % 3;
+          buf = ring + t < 3 ? ring + t : 0;
+        }
         bars->ml[t][row] = make_float2(m, l.x + l.y);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->ml_full[t]);

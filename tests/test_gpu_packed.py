@@ -635,3 +635,19 @@ def test_units_of_odd_numbers_of_steps(d):
     q = randn(cu[-1], Hkv * G, d, seed=103, scale=1.5)
     step = run_attend(q, mem, cu, lens, Hkv)
     check(step, exact(q, mem, cu, lens, True, G), max(lens), d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [1, 40, 300])
+def test_maxima_that_rise_at_every_step(d, new):
+    """Later keys are ever longer, so that O is rescaled at most steps, in some rows of a warp and
+    not in others."""
+    G, Hkv, n = 4, 2, 1400
+    mem = Paged([n], Hkv, d, seed=104)
+    pages = mem.pt[0].long()
+    for j, p in enumerate(pages[:-(-n // 64)].tolist()):
+        mem.K[p] = (mem.K[p].float() * (1.0 + 1.5 * j)).to(torch.bfloat16)
+    q = randn(new, Hkv * G, d, seed=105, scale=1.5)
+    q[::3] *= 0.05
+    step = run_attend(q, mem, [0, new], [n], Hkv)
+    check(step, exact(q, mem, [0, new], [n], True, G), n, d)
