@@ -414,7 +414,7 @@ BSA_DEVFN int unit_of_round(int k) {
 // One row over ten keys takes 9.3 us instead of 13.0 with the plan kernel, 32 rows behind 32K keys
 // 48 instead of 55, 693 rows over 3K keys (16/8 heads, d = 64) 43 and 47; where units that blocks
 // take when they are free would be better it loses (27 rows each of 16 sequences over 12K keys,
-// 64/4 heads: 122 and 114). Four rounds: 200 rows behind three prefixes 483 us, 378 with two.
+// 64/4 heads: 122 and 114, before rows that do not exist cost nothing). More rounds: the same.
 BSA_DEVFN int plan_in_warp(const PackedArgs& a, int4* own, int& more) {
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31;
@@ -504,14 +504,13 @@ BSA_DEVFN int plan_in_warp(const PackedArgs& a, int4* own, int& more) {
   for (int k = 0; k < kRounds; ++k) {
     const int u = unit_of_round(k);
     if (u >= units) break;
-    const bool by_head = !a.causal && units > static_cast<int>(gridDim.x);
-    const int e = by_head ? u % entries : u / a.Hkv, g = by_head ? u / entries : u % a.Hkv;
+    const int e = u / a.Hkv;
     const bool mine = n > 0 && at <= e && e < at + n;
     if (mine) {
       const int split = e - at;
       own[2 * k] = make_int4(x.b, x.row0, x.ntok, x.pos0);
       own[2 * k + 1] = make_int4(x.len, x.steps * split / n, x.steps * (split + 1) / n, split | (n << 16));
-      if (any && split == 0 && g == 0)
+      if (any && split == 0 && u % a.Hkv == 0)
         for (int i = 0; i < x.ntok; ++i) a.row_splits[x.row0 + i] = n;
     }
   }
@@ -751,27 +750,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (un > 0) u = a.in_block ? unit_of_round(un)
                                    : gridDim.x + __shfl_sync(0xffffffffu, next, 0);
         // The heads of an entry are neighbours: the longest units of all heads start first
-        // (prompts of 2K and 4K: 53 and 146 us, 69 and 168 with one head after the other), and
-        // an entry is read beside the number of entries. Without the causal limit units are
-        // alike, and one head comes after the other where they do not all run at once, so that
-        // the units at work share its keys through L2 (200 rows behind three prefixes of up to
-        // 64K: 399 us, 437 with the heads as neighbours).
-        int e = min(u / a.Hkv, a.max_entries - 1), g = u % a.Hkv;
+        // (prompts of 2K and 4K: 51 and 132 us, 67 and 155 with one head after the other; prefixes
+        // that many rows share: the same within 4%).
+        const int e = min(u / a.Hkv, a.max_entries - 1), g = u % a.Hkv;
         const int4* from = a.in_block ? bars->own + 2 * (un % kRounds) : a.entries + 2 * e;
-        int4 e0 = from[0], e1 = from[1];
+        const int4 e0 = from[0], e1 = from[1];
         if (un == 0) {
           units = a.in_block ? own_units : a.head[0] * a.Hkv;
           if (!a.in_block) more = a.head[3];
         }
         if (un == kRounds && a.in_block) units = 0;
-        if (!a.causal && units > static_cast<int>(gridDim.x) && u < units) {
-          g = u / (units / a.Hkv);
-          e = u - g * (units / a.Hkv);
-          if (!a.in_block) {
-            e0 = a.entries[2 * e];
-            e1 = a.entries[2 * e + 1];
-          }
-        }
         int rk = -1, rv = -1, nblk = 0;
         // the cache rows of the unit's blocks from `first`, one a lane: -1 behind the end, and
         // for a bad block
