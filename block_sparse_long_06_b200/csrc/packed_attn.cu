@@ -14,12 +14,12 @@
 //    rows gives both tiles of tensor memory the same rows and its steps in turn; their
 //    results are joined when they are written.
 //  * A step is 128 keys (two blocks of the cache). The loader warp copies K and V of a step
-//    into a ring of 32 KB stages; one issuing thread runs S = Q K^T into the tile's 128
-//    columns of tensor memory and O += P V from it; four softmax warps per tile, a thread a
-//    row, turn S into P, written as bf16 over S. The two tiles take turns:
-//    while one is in its softmax, the other has the tensor cores. P V (j) and S (j + 1) of a
-//    tile are issued by the same thread, in order, so S needs no second buffer and the
-//    arrival of S (j + 1) says that P V (j) is done.
+//    into a ring of 32 KB stages; one issuing thread runs S = Q K^T into 128 columns of tensor
+//    memory and O += P V from them; four softmax warps per tile, a thread a row, turn S into P,
+//    written as bf16 over S. The two tiles take turns: while one is in its softmax, the other
+//    has the tensor cores. P V (j) and S (j + 1) of a tile are issued by the same thread, in
+//    order, so S needs no second buffer and the arrival of S (j + 1) says that P V (j) is done.
+//    (At d = 64 there is room for a third buffer of scores, and S runs further ahead.)
 //  * The running maximum only moves when it grows by more than 8 (log2): O is then rescaled
 //    in tensor memory. P <= 2^8 is rounded to bf16 (at most 2^-8 of each term, as much as the
 //    output's own rounding, and averaged over a row's terms); l sums the fp32 values. V stays
@@ -33,8 +33,8 @@
 //  * Rows of V behind a sequence's end are whatever the page held before: a patch warp
 //    zeroes them in shared memory in the step that has the end (0 * NaN is NaN), before the
 //    step is handed to the tensor cores. K there may be anything: its scores are replaced.
-// Tensor memory: O of tile t at d t, the scores' buffers (then P) of 128 columns from 2 d. Every wait is
-// bounded; on a timeout the kernel reports BSA_DEV_TIMEOUT, drains and returns.
+// Tensor memory: O of tile t at d t, the scores' buffers (then P) of 128 columns from 2 d. Every
+// wait is bounded; on a timeout the kernel reports BSA_DEV_TIMEOUT, drains and returns.
 #include <algorithm>
 
 #include "tcgen05.cuh"
