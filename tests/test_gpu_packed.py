@@ -651,3 +651,65 @@ def test_maxima_that_rise_at_every_step(d, new):
     q[::3] *= 0.05
     step = run_attend(q, mem, [0, new], [n], Hkv)
     check(step, exact(q, mem, [0, new], [n], True, G), n, d)
+
+
+@pytest.mark.parametrize("B,shared", [(3, False), (40, False), (3, True), (40, True)])
+def test_a_captured_plan_follows_the_lengths(B, shared):
+    """Splits, rows and the number of tiles change from replay to replay, in both ways to plan; an
+    outsider's results with the same lengths are the same bits."""
+    d, G, Hkv, T = 128, 4, 2, 4096
+    N = 4 * B
+    mem = Paged([T] * B, Hkv, d, seed=110, T=T)
+    q = randn(N, Hkv * G, d, seed=111, scale=1.5)
+    own = ()
+    if shared:
+        own = (torch.randn(N, Hkv * G, d, generator=gen(112), device="cuda"),
+               8.0 + torch.randn(N, Hkv * G, generator=gen(113), device="cuda"))
+    cu, lens = ints([4 * b for b in range(B + 1)]), ints([T] * B)
+    make = bsa.SharedPrefixDecode if shared else bsa.PackedAttention
+    tok = lambda c, n: bsa.Tokens(N=N, B=B, Hq=Hkv * G, Hkv=Hkv, d=d, T=T, cu_seqlens=c, seq_lens=n)
+    step = make(tok(cu, lens))
+    caches = mem.caches()
+    step.run(q, *caches, *own)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step.run(q, *caches, *own)
+    for seed in range(4):
+        r = np.random.default_rng(seed)
+        rows = [0, 1, 4, 2][seed] + r.integers(0, 1 + [4, 3, 0, 1][seed], B)
+        have = r.integers(4, [T, 200, T, 1500][seed] + 1, B)
+        cu.copy_(ints(sums(rows.tolist())))
+        lens.copy_(ints(have.tolist()))
+        for x in (step.o, step.lse, step.o_f32):
+            x.fill_(77.0)
+        graph.replay()
+        other = make(tok(cu.clone(), lens.clone()))
+        for x in (other.o, other.lse, other.o_f32):
+            x.fill_(77.0)
+        other.run(q, *caches, *own)
+        assert int(step.status.item()) == 0 and int(other.status.item()) == 0
+        for a, b in ((step.o, other.o), (step.lse, other.lse), (step.o_f32, other.o_f32)):
+            assert torch.equal(a, b)
+        n = int(rows.sum())
+        assert (step.lse[n:] == 77.0).all() and (step.lse[:n] != 77.0).all()
+    # the last batch against 64 bits
+    c = sums(rows.tolist())
+    want = (exact_shared(q, mem, c, have.tolist(), G, own) if shared
+            else exact(q, mem, c, have.tolist(), True, G))
+    check(step, want, T, d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_own_part_in_place_with_and_without_splits(d):
+    """o_f32 is o_own and lse is lse_own, for rows that the merge writes and rows that it does not."""
+    G, Hkv, rows, lens = 4, 2, [3, 5, 70], [6000, 100, 3001]
+    cu = sums(rows)
+    mem = Paged(lens, Hkv, d, seed=120)
+    q = randn(cu[-1], Hkv * G, d, seed=121, scale=1.5)
+    o_own = torch.randn(cu[-1], Hkv * G, d, generator=gen(122), device="cuda")
+    lse_own = 8.0 + torch.randn(cu[-1], Hkv * G, generator=gen(123), device="cuda")
+    step = run_shared(q, mem, cu, lens, Hkv, (o_own, lse_own))
+    check(step, exact_shared(q, mem, cu, lens, G, (o_own, lse_own)), max(lens), d)
+    bsa.bsa_decode_shared(step.tok, q, *mem.caches(), o_own, lse_own, step.o, lse_own, o_own,
+                          step.workspace, step.status)
+    assert torch.equal(o_own, step.o_f32) and torch.equal(lse_own, step.lse)
