@@ -611,10 +611,15 @@ def _packed_call(name, tok, q, k, v, own, o, lse, o_f32, workspace, dev_status, 
     dev = q.get_device()
     N, Hq, d = tok.N, tok.Hq, tok.d
     stride = q.stride()
-    if q.dtype != torch.bfloat16 or q.shape != (N, Hq, d) or dev < 0 or (
+    if q.dtype != torch.bfloat16 or q.shape != (N, Hq, d) or (
             N > 0 and (stride[2] != 1 or stride[1] != d)):
-        raise BsaError(f"{name}: q has to be bfloat16 [{N}, {Hq}, {d}] on the GPU, a token's "
-                       f"heads side by side, got {q.dtype} {tuple(q.shape)} {q.stride()}")
+        raise BsaError(f"{name}: q has to be bfloat16 [{N}, {Hq}, {d}], a token's heads side by "
+                       f"side, got {q.dtype} {tuple(q.shape)} {q.stride()}")
+    if N > 1 and stride[0] < Hq * d:      # (0 in the struct is the default, not one row for all)
+        raise BsaError(f"{name}: q's rows overlap: {stride[0]} elements between tokens, wanted "
+                       f"{Hq * d} at least")
+    if dev < 0:
+        raise BsaError(f"{name}: q has to be on the GPU")
     c = _tokens_on(tok, dev)
     _check_device(dev, k.tensor, k.page_table, v.tensor, v.page_table, o, lse, o_f32, workspace,
                   dev_status, *own)

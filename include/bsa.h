@@ -330,7 +330,7 @@ typedef struct {
                                 0: it sees its whole sequence */
   float attn_scale;          /* softmax scale; 0 = 1/sqrt(d) */
   int64_t q_stride;          /* attention: elements between the query rows of two tokens
-                                (a multiple of 8); 0 = Hq*d */
+                                (a multiple of 8, at least Hq*d); 0 = Hq*d */
 } bsa_tokens_t;
 
 /* Head norm and rotary positions. For each row and each head of q and k (width d):

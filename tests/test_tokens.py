@@ -251,3 +251,21 @@ def test_python_checks_raise_before_the_library():
     with pytest.raises(bsa.BsaError):
         bsa.Tokens(N=2, B=2, Hq=4, Hkv=2, d=64, T=64,
                    seq_lens=torch.zeros(2, dtype=torch.int64)).c()
+
+
+# ------------------------------------------------------------------ queries of the binding
+def test_queries_whose_rows_overlap_are_refused():
+    """A stride of 0 would be taken for the default, rows behind the buffer's end for queries."""
+    tok = bsa.Tokens(N=3, B=3, Hq=4, Hkv=2, d=64, T=64)
+    one = torch.zeros(1, 4, 64, dtype=torch.bfloat16)
+    close = torch.zeros(2 * 128 + 256, dtype=torch.bfloat16).as_strided((3, 4, 64), (128, 64, 1))
+    c = bsa.contiguous_cache(torch.zeros(3, 2, 64, 64, dtype=torch.bfloat16))
+    for call in (lambda q: bsa.bsa_attend_packed(tok, q, c, c, None, None, None, None),
+                 lambda q: bsa.bsa_decode_shared(tok, q, c, c, None, None, None, None, None, None)):
+        for q in (one.expand(3, 4, 64), close):
+            with pytest.raises(bsa.BsaError, match="overlap"):
+                call(q)
+        for q in (torch.zeros(3, 4, 64, dtype=torch.bfloat16),
+                  torch.zeros(3, 8, 64, dtype=torch.bfloat16)[:, 2:6]):
+            with pytest.raises(bsa.BsaError, match="GPU"):
+                call(q)
