@@ -215,22 +215,30 @@ class Cache:
     page_table: Optional[torch.Tensor] = None
     num_pages: int = 0
 
+    _kept = None                               # the last call's struct, not part of the state
+
     def __setattr__(self, name, value):
-        # the struct is kept between calls until a field changes
         object.__setattr__(self, name, value)
         if name != "_kept":
             object.__setattr__(self, "_kept", None)
 
-    def c(self) -> CCache:
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_kept"}
+
+    def _struct(self) -> CCache:
+        """The struct kept between calls until a field changes: for one call, by value. What a
+        tensor says of itself (address, sizes) is read every time."""
         pt, c = self.page_table, self._kept
         if c is None:
             c = self._kept = CCache(None, self.seq_stride, self.block_stride, self.head_stride,
-                                    None, 0 if pt is None else pt.shape[1], self.num_pages,
-                                    self.tensor.numel())
-        c.base = self.tensor.data_ptr()
+                                    None, 0, self.num_pages, 0)
+        c.base, c.extent = self.tensor.data_ptr(), self.tensor.numel()
         if pt is not None:
-            c.page_table = pt.data_ptr()
+            c.page_table, c.page_table_stride = pt.data_ptr(), pt.shape[1]
         return c
+
+    def c(self) -> CCache:
+        return CCache.from_buffer_copy(self._struct())
 
 
 def contiguous_cache(t: torch.Tensor) -> Cache:
@@ -370,14 +378,15 @@ class Tokens:
     r: int = 16
     block: int = BLOCK
 
-    def __post_init__(self):
-        self._kept = None
+    _kept = None                               # the last call's description, not part of the state
 
     def __setattr__(self, name, value):
-        # the checked description is kept between calls until a field changes
         object.__setattr__(self, name, value)
         if name != "_kept":
             object.__setattr__(self, "_kept", None)
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_kept"}
 
     def tensors(self):
         rope = self.rope
@@ -385,22 +394,31 @@ class Tokens:
                 None if rope is None else rope.steps)
 
     def _description(self):
-        """(struct, device index or -1): checked once, then only the addresses are renewed."""
+        """(struct, device index or -1), kept between calls until a field changes: for one call, by
+        value. Checked once, and again where a tensor has another size or device."""
         kept, rope = self._kept, self.rope
         if kept is None or (rope is not None and (kept[3] is not rope.steps or
                                                   kept[4] != (rope.interleaved, rope.factor))):
-            names = ("cu_seqlens", "seq_lens", "positions", "q_weight", "k_weight", "rope_steps")
-            given = [(n, t) for n, t in zip(names, self.tensors()) if t is not None]
-            kept = self._kept = (self._describe(), given[0][1].get_device() if given else -1, given,
-                                 None if rope is None else rope.steps,
-                                 None if rope is None else (rope.interleaved, rope.factor))
-        c = kept[0]
-        for name, t in kept[2]:
+            kept = self._describe_again()
+        c, at = kept[0], kept[1]
+        for name, t, n in kept[2]:
+            if t.numel() != n or t.get_device() != at:
+                self._describe_again()
+                return self._description()
             setattr(c, name, t.data_ptr())
-        return c, kept[1]
+        return c, at
+
+    def _describe_again(self):
+        self._kept, rope = None, self.rope
+        names = ("cu_seqlens", "seq_lens", "positions", "q_weight", "k_weight", "rope_steps")
+        given = [(n, t, t.numel()) for n, t in zip(names, self.tensors()) if t is not None]
+        self._kept = (self._describe(), given[0][1].get_device() if given else -1, given,
+                      None if rope is None else rope.steps,
+                      None if rope is None else (rope.interleaved, rope.factor))
+        return self._kept
 
     def c(self) -> CTokens:
-        return self._description()[0]
+        return CTokens.from_buffer_copy(self._description()[0])
 
     def _describe(self) -> CTokens:
         _want("cu_seqlens", self.cu_seqlens, torch.int32, (self.B + 1,))
@@ -431,8 +449,12 @@ def _want(name, t, dtype, shape):
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise BsaError(f"{name}: contiguous {dtype} {tuple(shape)} wanted, got {t.dtype} "
                        f"{tuple(t.shape)} with strides {t.stride()}")
-    if not t.is_cuda:
+    if not _on_gpu(t):
         raise BsaError(f"{name}: has to be on the GPU")
+
+
+def _on_gpu(t):
+    return t.is_cuda
 
 
 _NO_ROWS = CRows(None, 0, 0, 0)
@@ -594,8 +616,8 @@ def bsa_append_kv(tok: Tokens, k, v, k_cache: Cache, v_cache: Cache, k_idx=None,
         _check_device(dev, kidx_cache.tensor, kidx_cache.page_table)
     _launch(load_library().bsa_append_kv, "bsa_append_kv", dev, c,
             _rows("k", k, N, H, d, dev), _rows("v", v, N, H, d, dev),
-            _rows("k_idx", k_idx, N, H, tok.r, dev), k_cache.c(), v_cache.c(),
-            CCache() if kidx_cache is None else kidx_cache.c(),
+            _rows("k_idx", k_idx, N, H, tok.r, dev), k_cache._struct(), v_cache._struct(),
+            CCache() if kidx_cache is None else kidx_cache._struct(),
             _rows("q", q, N, tok.Hq, d, dev), _rows("q_out", q_out, N, tok.Hq, d, dev, True),
             None if dev_status is None else dev_status.data_ptr(), _raw_stream(stream, dev))
 
@@ -632,7 +654,7 @@ def _packed_call(name, tok, q, k, v, own, o, lse, o_f32, workspace, dev_status, 
         if stride[0] != Hq * d:
             c = CTokens.from_buffer_copy(c)
             c.q_stride = stride[0]
-    args = [c, q.data_ptr(), k.c(), v.c()]
+    args = [c, q.data_ptr(), k._struct(), v._struct()]
     if own:
         _want("o_own", own[0], torch.float32, (N, Hq, d))
         _want("lse_own", own[1], torch.float32, (N, Hq))

@@ -1,7 +1,9 @@
 """Operators around the caches, on the CPU: rotary tables against 64-bit angles, the oracle's
 pins, and the arguments that the entry points refuse before any launch."""
+import copy
 import ctypes
 import math
+import pickle
 
 import numpy as np
 import pytest
@@ -269,3 +271,51 @@ def test_queries_whose_rows_overlap_are_refused():
                   torch.zeros(3, 8, 64, dtype=torch.bfloat16)[:, 2:6]):
             with pytest.raises(bsa.BsaError, match="GPU"):
                 call(q)
+
+
+# ------------------------------------------------------------------ structs of the binding
+def test_described_caches_and_tokens_can_be_copied():
+    pool = torch.zeros(3, 2, 64, 16, dtype=torch.bfloat16)
+    c = bsa.paged_cache(pool, torch.zeros(2, 4, dtype=torch.int32))
+    tok = bsa.Tokens(N=2, B=2, Hq=4, Hkv=2, d=64, T=64, eps=0.5)
+    before = bytes(c.c()), bytes(tok.c())
+    for one in (copy.deepcopy(c), copy.copy(c), pickle.loads(pickle.dumps(c))):
+        struct = one.c()
+        assert struct.base == one.tensor.data_ptr()
+        assert struct.page_table == one.page_table.data_ptr() and struct.page_table_stride == 4
+    for one in (copy.deepcopy(tok), copy.copy(tok), pickle.loads(pickle.dumps(tok))):
+        one.N = 1
+        assert one.c().N == 1 and one.c().eps == 0.5
+    assert (bytes(c.c()), bytes(tok.c())) == before
+
+
+def test_structs_are_the_callers_own():
+    c = bsa.contiguous_cache(torch.zeros(1, 2, 64, 16, dtype=torch.bfloat16))
+    tok = bsa.Tokens(N=2, B=2, Hq=4, Hkv=2, d=64, T=64)
+    for what, name in ((c, "extent"), (tok, "N")):
+        one, other = what.c(), what.c()
+        setattr(one, name, 1 << 20)
+        assert getattr(other, name) == getattr(what.c(), name) != 1 << 20
+
+
+def test_sizes_follow_tensors_changed_in_place():
+    pool, table = torch.zeros(8, 2, 64, 16, dtype=torch.bfloat16), torch.zeros(2, 6, dtype=torch.int32)
+    c = bsa.paged_cache(pool, table)
+    for struct in (c.c, c._struct):
+        assert struct().extent == pool.numel() and struct().page_table_stride == 6
+    pool.resize_(3, 2, 64, 16)
+    table.resize_(2, 3)
+    for struct in (c.c, c._struct):
+        assert struct().extent == 3 * 2 * 64 * 16 and struct().page_table_stride == 3
+    c.tensor.data = torch.zeros(1, 2, 64, 16, dtype=torch.bfloat16)
+    assert c._struct().extent == 2 * 64 * 16 and c._struct().base == c.tensor.data_ptr()
+
+
+def test_lengths_changed_in_place_are_checked_again(monkeypatch):
+    monkeypatch.setattr(bsa, "_on_gpu", lambda t: True)
+    lens = torch.zeros(2, dtype=torch.int32)
+    tok = bsa.Tokens(N=2, B=2, Hq=4, Hkv=2, d=64, T=64, seq_lens=lens)
+    assert tok.c().seq_lens == lens.data_ptr()
+    lens.resize_(1)
+    with pytest.raises(bsa.BsaError, match="seq_lens"):
+        tok.c()
