@@ -798,7 +798,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int end = min(2 * U.step1, nblk), from = 2 * U.step0 + 32;
           if (from < end) {
             bool later = scan(a.k, a.k_safe, U, from + lane, end);
-            if (a.v.page_table != a.k.page_table || !a.k_safe || !a.v_safe || a.v.num_pages < a.k.num_pages)
+            if (a.v.page_table != a.k.page_table || a.v.pt_stride != a.k.pt_stride || !a.k_safe || !a.v_safe ||
+                a.v.num_pages < a.k.num_pages)
               later |= scan(a.v, a.v_safe, U, from + lane, end);
             bad |= __any_sync(0xffffffffu, later) != 0;
           }

@@ -713,3 +713,37 @@ def test_own_part_in_place_with_and_without_splits(d):
     bsa.bsa_decode_shared(step.tok, q, *mem.caches(), o_own, lse_own, step.o, lse_own, o_own,
                           step.workspace, step.status)
     assert torch.equal(o_own, step.o_f32) and torch.equal(lse_own, step.lse)
+
+
+@pytest.mark.parametrize("new", [1, 70])
+def test_bad_value_pages_of_a_table_with_rows_of_its_own(new):
+    """K's and V's tables start at the same address, V's rows are closer together: a bad page of
+    V's alone, behind the first 32 blocks, is found as one of K's is."""
+    d, G, Hkv, nb = 64, 4, 2, 40
+    n = nb * 64 - 5
+    K, V = randn(2 * nb, Hkv, 64, d, seed=130), randn(2 * nb, Hkv, 64, d, seed=131)
+    table = torch.full((4 * nb,), -1, dtype=torch.int32)
+    kt, vt = table.view(2, 2 * nb), table[:2 * nb].view(2, nb)
+    kt[0, :nb], kt[1, :nb] = torch.arange(nb), torch.arange(nb, 2 * nb)
+    vt[1] = torch.arange(nb).flip(0)
+    table[nb + 35] = 1 << 20                        # block 35 of V's second sequence
+    table = table.cuda()
+    kt, vt = table.view(2, 2 * nb), table[:2 * nb].view(2, nb)
+    caches = bsa.paged_cache(K, kt), bsa.paged_cache(V, vt)
+    assert kt.data_ptr() == vt.data_ptr()
+    cu = [0, new, 2 * new]
+    q = randn(2 * new, Hkv * G, d, seed=132, scale=1.5)
+    tok = bsa.Tokens(N=2 * new, B=2, Hq=Hkv * G, Hkv=Hkv, d=d, T=nb * 64, cu_seqlens=ints(cu),
+                     seq_lens=ints([n, n]))
+    step = bsa.PackedAttention(tok)
+    step.run(q, *caches)
+    assert int(step.status.item()) == bsa.BSA_DEV_BAD_PAGE
+
+    class Two:
+        pass
+    mem = Two()
+    mem.K, mem.V = K, V
+    mem.keys = lambda X, b, m: f64(X[(kt if X is K else vt)[b, :nb].long().clamp(max=2 * nb - 1)]).transpose(
+        1, 0, 2, 3).reshape(Hkv, -1, d)[:, :m]
+    hide = lambda b, j: (j // 64 == 35) if b == 1 else np.zeros(len(j), bool)
+    check(step, exact(q, mem, cu, [n, n], True, G, hide=hide), n, d)
