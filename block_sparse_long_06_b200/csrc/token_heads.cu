@@ -143,8 +143,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(In) == 4 ? 3 : 4) token_heads
       kslot = slot_of(a.k_cache, b, static_cast<int>(token), a.Hkv, D);
       vslot = slot_of(a.v_cache, b, static_cast<int>(token), a.Hkv, D);
       if (a.kidx.base != nullptr) xslot = slot_of(a.kidx_cache, b, static_cast<int>(token), a.Hkv, kR);
-      if (lane == 0 && (kslot < 0 || vslot < 0 || (a.kidx.base != nullptr && xslot < 0)))
-        report(a.status, BSA_DEV_BAD_PAGE);
+      if (kslot < 0 || vslot < 0 || (a.kidx.base != nullptr && xslot < 0)) {
+        if (lane == 0) report(a.status, BSA_DEV_BAD_PAGE);
+        kslot = vslot = xslot = -1;              // all of a token's slots or none
+      }
     }
     if (a.positions == nullptr) pos = token;
   }

@@ -258,3 +258,39 @@ def test_append_replays_in_a_graph_with_new_lengths():
     f, _ = bsa.rope_frequencies(d)
     y = TO.norm_rope(f64(k), [29, 64, 127], f)
     close(torch.stack([K[0, :, 29], K[3, :, 0], K[5, :, 63]]), *y)
+
+
+@pytest.mark.parametrize("bad", ["K", "V", "I", "extent"])
+def test_append_writes_all_caches_or_none(bad):
+    """Tables of their own for K, V and index keys, one of them with a page that does not exist
+    (or a pool that ends before it): the row's other slots stay as they were, its query comes."""
+    B, H, d = 3, 2, 128
+    q, k, v = qkv_rows(B, 4, H, d, torch.bfloat16, 18)
+    idx = torch.randn(B, H, 16, generator=gen(19), device="cuda").to(torch.bfloat16)
+    pool = dict(zip("KVI", pools(6, H, d, 20)))
+    table = dict(K=ints([[0, 1], [2, 3], [4, 5]]), V=ints([[5, 4], [3, 2], [1, 0]]),
+                 I=ints([[2, 3], [4, 5], [0, 1]]))
+    if bad in table:
+        table[bad][1, 1] = 77
+    caches = {n: bsa.paged_cache(pool[n], table[n]) for n in "KVI"}
+    if bad == "extent":           # the index keys' page 5 (sequence 1) is cut off
+        caches["I"] = bsa.paged_cache(pool["I"][:5], table["I"])
+        caches["I"].num_pages = 6
+    before = {n: x.clone() for n, x in pool.items()}
+    tok = bsa.Tokens(N=B, B=B, Hq=4, Hkv=H, d=d, T=128, seq_lens=ints([3, 70, 128]),
+                     rope=bsa.Rope.make(d))
+    q_out = torch.zeros(B, 4, d, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    bsa.bsa_append_kv(tok, k, v, caches["K"], caches["V"], idx, caches["I"], q, q_out, status)
+    assert int(status.item()) == bsa.BSA_DEV_BAD_PAGE
+    f, _ = bsa.rope_frequencies(d)
+    close(q_out, *TO.norm_rope(f64(q), [2, 69, 127], f))
+    want = TO.norm_rope(f64(k), [2, 69, 127], f)
+    for b, pos in ((0, 2), (2, 127)):
+        at = {n: (int(table[n][b, pos // 64]), slice(None), pos % 64) for n in "KVI"}
+        close(pool["K"][at["K"]], want[0][b], want[1][b])
+        assert torch.equal(pool["V"][at["V"]], v[b]) and torch.equal(pool["I"][at["I"]], idx[b])
+        for n in "KVI":
+            pool[n][at[n]] = before[n][at[n]]
+    for n in "KVI":
+        assert torch.equal(pool[n], before[n])
