@@ -231,11 +231,17 @@ bsa_status_t check_rows(const bsa_rows_t& x, int type) {
   return BSA_OK;
 }
 
-// Output rows (bf16) of N tokens and `heads` heads: heads may not overlap.
+// Output rows (bf16) of N tokens and `heads` heads: no two overlap, with a token's heads between
+// those of other tokens or the other way round.
 bsa_status_t check_out(const bsa_rows_t& x, const bsa_tokens_t* t, int heads) {
   bsa_status_t st = check_rows(x, BSA_TYPE_BF16);
   if (st != BSA_OK) return st;
   if ((t->N > 1 && x.token_stride < t->d) || (heads > 1 && x.head_stride < t->d))
+    return BSA_ERR_INVALID_ARG;
+  // in 128 bits: the strides are the caller's
+  if (t->N > 1 && heads > 1 &&
+      x.token_stride < static_cast<__int128>(heads - 1) * x.head_stride + t->d &&
+      x.head_stride < static_cast<__int128>(t->N - 1) * x.token_stride + t->d)
     return BSA_ERR_INVALID_ARG;
   return BSA_OK;
 }

@@ -297,7 +297,9 @@ typedef enum { BSA_TYPE_BF16 = 0, BSA_TYPE_F16 = 1, BSA_TYPE_F32 = 2 } bsa_type_
 /* Head rows in memory: element c of head h of row n is element
  * n*token_stride + h*head_stride + c from `base`; the elements of one head are
  * contiguous and start on a 16-byte boundary (base and strides). A stride of 0 reads
- * one row for all; the heads of an output may not overlap. base = NULL: none. */
+ * one row for all. An output's heads may not overlap: either a token's heads all lie
+ * before the next token's, or a head's tokens all before the next head's. base = NULL:
+ * none. */
 typedef struct {
   void* base;
   int64_t token_stride;      /* elements */

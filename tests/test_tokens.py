@@ -319,3 +319,17 @@ def test_lengths_changed_in_place_are_checked_again(monkeypatch):
     lens.resize_(1)
     with pytest.raises(bsa.BsaError, match="seq_lens"):
         tok.c()
+
+
+# ------------------------------------------------------------------ what is written, once
+def test_outputs_whose_rows_overlap_are_refused(lib):
+    """Head h + 1 of a row may not be head h of the next, in no order of rows and heads."""
+    E = bsa.BSA_ERR_INVALID_ARG
+    two = lambda **kw: ctypes.byref(tokens(**kw))           # N = 4 rows, 8 and 2 heads, d = 128
+    for bad in (rows(0x20000, ts=128, hs=128), rows(0x20000, ts=1016, hs=128),
+                rows(0x20000, ts=128, hs=504), rows(0x20000, ts=256, hs=128)):
+        assert lib.bsa_norm_rope(two(), rows(), bad, NONE, NONE, None, None) == E
+        assert lib.bsa_append_kv(two(), rows(), rows(), NONE, cache(), cache(), bsa.CCache(),
+                                 rows(), bad, None, None) == E
+    assert lib.bsa_norm_rope(two(), NONE, NONE, rows(), rows(0x20000, ts=128, hs=128), None,
+                             None) == E
