@@ -259,6 +259,36 @@ bsa_status_t check_token_cache(const bsa_cache_t& c, const bsa_tokens_t* t, int 
   return check_cache(c, &p, width, rows_tma);
 }
 
+// Cache checks for appends: besides, no two token slots overlap (a token of the capacity T behind
+// the end of its head's rows would land in the next head's). Each stride of the nest, from the
+// smallest, has to span what lies inside it. Sequences of a page table share the pool, where the
+// table says who has which page, unless seq_stride gives them one each.
+bsa_status_t check_append_cache(const bsa_cache_t& c, const bsa_tokens_t* t, int width, bool rows_tma) {
+  const bsa_status_t st = check_token_cache(c, t, width, rows_tma);
+  if (st != BSA_OK || t->T == 0) return st;
+  const bool paged = c.page_table != nullptr;
+  struct Dim {
+    int64_t count, stride;
+    bool blocks;
+  } dims[3] = {{paged ? c.num_pages : nblocks(t->T), c.block_stride, true},
+               {t->Hkv, c.head_stride, false},
+               {paged && c.seq_stride == 0 ? 1 : t->B, c.seq_stride, false}};
+  std::sort(dims, dims + 3, [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
+  __int128 span = static_cast<__int128>(paged ? 64 : std::min(64, t->T)) * width;
+  const __int128 block = span;
+  for (const Dim& x : dims) {
+    if (x.count <= 1) continue;
+    if (x.stride < span) return BSA_ERR_INVALID_ARG;
+    const __int128 last = static_cast<__int128>(x.count - 1) * x.stride;
+    // the last block of a head's rows may be a part
+    if (x.blocks && !paged && span == block)
+      span = last + static_cast<__int128>(t->T - (x.count - 1) * 64) * width;
+    else
+      span += last;
+  }
+  return BSA_OK;
+}
+
 bsa::RowsView rows_view(const bsa_rows_t& x) {
   bsa::RowsView v;
   v.base = x.base;
@@ -853,8 +883,8 @@ bsa_status_t bsa_append_kv(const bsa_tokens_t* t, bsa_rows_t k, bsa_rows_t v, bs
   if (type != BSA_TYPE_BF16 && type != BSA_TYPE_F16 && type != BSA_TYPE_F32)
     return BSA_ERR_INVALID_ARG;
   if ((st = check_rows(k, type)) != BSA_OK || (st = check_rows(v, type)) != BSA_OK) return st;
-  if ((st = check_token_cache(k_cache, t, t->d, true)) != BSA_OK) return st;
-  if ((st = check_token_cache(v_cache, t, t->d, true)) != BSA_OK) return st;
+  if ((st = check_append_cache(k_cache, t, t->d, true)) != BSA_OK) return st;
+  if ((st = check_append_cache(v_cache, t, t->d, true)) != BSA_OK) return st;
   bsa::HeadsArgs a = heads_args(t, type, dev_status);
   a.k = rows_view(k);
   a.v = rows_view(v);
@@ -862,7 +892,7 @@ bsa_status_t bsa_append_kv(const bsa_tokens_t* t, bsa_rows_t k, bsa_rows_t v, bs
   a.v_cache = view(v_cache);
   if (kidx.base != nullptr) {
     if ((st = check_rows(kidx, type)) != BSA_OK) return st;
-    if ((st = check_token_cache(kidx_cache, t, t->r, false)) != BSA_OK) return st;
+    if ((st = check_append_cache(kidx_cache, t, t->r, false)) != BSA_OK) return st;
     a.kidx = rows_view(kidx);
     a.kidx_cache = view(kidx_cache);
   }

@@ -350,8 +350,9 @@ bsa_status_t bsa_norm_rope(const bsa_tokens_t* tok, bsa_rows_t q, bsa_rows_t q_o
  * token's slot of k_cache, v_cache and kidx_cache. Where q.base is not NULL its heads
  * are normed and rotated into q_out by the same launch. A row whose slot does not
  * exist in one of the caches (bad page, outside the extent) is reported and written into
- * none of them; its q heads are. Two rows with
- * the same slot (a page that two sequences share) leave a mixture of both. */
+ * none of them; its q heads are. Slots of tokens below T may not overlap (a contiguous
+ * cache has T tokens a head at least). Two rows with the same slot (a page that two
+ * sequences share) leave a mixture of both. */
 bsa_status_t bsa_append_kv(const bsa_tokens_t* tok, bsa_rows_t k, bsa_rows_t v, bsa_rows_t kidx,
                            bsa_cache_t k_cache, bsa_cache_t v_cache, bsa_cache_t kidx_cache,
                            bsa_rows_t q, bsa_rows_t q_out, int32_t* dev_status, void* stream);

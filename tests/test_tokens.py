@@ -333,3 +333,53 @@ def test_outputs_whose_rows_overlap_are_refused(lib):
                                  rows(), bad, None, None) == E
     assert lib.bsa_norm_rope(two(), NONE, NONE, rows(), rows(0x20000, ts=128, hs=128), None,
                              None) == E
+
+
+W, T = 128, 200                                  # B = 2, Hkv = 2
+LAYOUTS = [
+    # (fits, cache fields): head by head, of T tokens or more
+    (True, dict(T=T)), (True, dict(T=256)), (False, dict(T=100)), (False, dict(T=199)),
+    # block by block, heads inside
+    (True, dict(block_stride=2 * 64 * W, head_stride=64 * W, seq_stride=8 * 64 * W)),
+    (False, dict(block_stride=2 * 64 * W, head_stride=64 * W, seq_stride=7 * 64 * W)),
+    (False, dict(block_stride=2 * 64 * W, head_stride=63 * W, seq_stride=8 * 64 * W)),
+    # sequence inside head
+    (True, dict(block_stride=64 * W, seq_stride=T * W, head_stride=2 * T * W)),
+    (False, dict(block_stride=64 * W, seq_stride=T * W, head_stride=T * W)),
+    (False, dict(seq_stride=0, T=T)), (False, dict(block_stride=63 * W, T=T)),
+    # pages: sequences share the pool, unless they have one each
+    (True, dict(page_table=0x5000, page_table_stride=4, num_pages=9, seq_stride=0,
+                block_stride=2 * 64 * W, head_stride=64 * W)),
+    (True, dict(page_table=0x5000, page_table_stride=4, num_pages=9, seq_stride=0,
+                block_stride=64 * W, head_stride=9 * 64 * W)),
+    (False, dict(page_table=0x5000, page_table_stride=4, num_pages=9, seq_stride=0,
+                 block_stride=64 * W, head_stride=64 * W)),
+    (False, dict(page_table=0x5000, page_table_stride=4, num_pages=9, seq_stride=8 * 2 * 64 * W,
+                 block_stride=2 * 64 * W, head_stride=64 * W)),
+]
+
+
+@pytest.mark.parametrize("fits,kw", LAYOUTS)
+def test_appends_go_into_caches_whose_slots_are_apart(lib, fits, kw):
+    """A token of the capacity T behind the end of its head's rows would overwrite the next
+    head's. Where K's layout is fine, V's size is what is refused."""
+    large = cache(extent=(1 << 31) * 128, T=256)
+    k = cache(extent=1 << 30, **kw)
+    t = ctypes.byref(tokens(T=T))
+    got = lib.bsa_append_kv(t, rows(), rows(), NONE, k, large, bsa.CCache(), NONE, NONE, None, None)
+    assert got == (bsa.BSA_ERR_UNSUPPORTED if fits else bsa.BSA_ERR_INVALID_ARG)
+
+
+def test_appends_check_values_and_index_keys_too(lib):
+    app, E = lib.bsa_append_kv, bsa.BSA_ERR_INVALID_ARG
+    t = ctypes.byref(tokens(T=T))
+    good, short = cache(T=256), cache(T=100, extent=1 << 30)
+    assert app(t, rows(), rows(), NONE, good, short, bsa.CCache(), NONE, NONE, None, None) == E
+    assert app(t, rows(), rows(), rows(), good, good, cache(width=16, T=100, extent=1 << 30), NONE,
+               NONE, None, None) == E
+    # capacity 0 has no slots, one sequence and one head no neighbours
+    large = cache(extent=(1 << 31) * 128)
+    for kw in (dict(T=0), dict(B=1, N=4, Hkv=1, Hq=8, T=256)):
+        assert app(ctypes.byref(tokens(**kw)), rows(), rows(), NONE, cache(T=64, head_stride=0, seq_stride=0,
+                   extent=1 << 20), large, bsa.CCache(), NONE, NONE, None,
+                   None) == bsa.BSA_ERR_UNSUPPORTED
