@@ -205,6 +205,9 @@ class Problem:
                         int(self.k_groups), _ptr(self.group_scores), _ptr(self.kept_groups))
 
 
+_I32 = torch.int32
+
+
 @dataclass
 class Cache:
     """A bf16 cache tensor (K, V or index keys) and its addressing (bsa_cache_t)."""
@@ -225,16 +228,17 @@ class Cache:
     def __getstate__(self):
         return {k: v for k, v in self.__dict__.items() if k != "_kept"}
 
-    def _struct(self) -> CCache:
+    def _struct(self, table=None) -> CCache:
         """The struct kept between calls until a field changes: for one call, by value. What a
-        tensor says of itself (address, sizes) is read every time."""
-        pt, c = self.page_table, self._kept
+        tensor says of itself is read every time. table: what _table says of the page table."""
+        c = self._kept
         if c is None:
             c = self._kept = CCache(None, self.seq_stride, self.block_stride, self.head_stride,
                                     None, 0, self.num_pages, 0)
         c.base, c.extent = self.tensor.data_ptr(), self.tensor.numel()
-        if pt is not None:
-            c.page_table, c.page_table_stride = pt.data_ptr(), pt.shape[1]
+        if self.page_table is not None:
+            c.page_table, c.page_table_stride = table or (self.page_table.data_ptr(),
+                                                          self.page_table.shape[1])
         return c
 
     def c(self) -> CCache:
@@ -395,18 +399,18 @@ class Tokens:
 
     def _description(self):
         """(struct, device index or -1), kept between calls until a field changes: for one call, by
-        value. Checked once, and again where a tensor has another size or device."""
+        value. Checked once, and again where a tensor has another size."""
         kept, rope = self._kept, self.rope
         if kept is None or (rope is not None and (kept[3] is not rope.steps or
                                                   kept[4] != (rope.interleaved, rope.factor))):
             kept = self._describe_again()
-        c, at = kept[0], kept[1]
+        c = kept[0]
         for name, t, n in kept[2]:
-            if t.numel() != n or t.get_device() != at:
+            if t.numel() != n:
                 self._describe_again()
                 return self._description()
             setattr(c, name, t.data_ptr())
-        return c, at
+        return c, kept[1]
 
     def _describe_again(self):
         self._kept, rope = None, self.rope
@@ -455,6 +459,35 @@ def _want(name, t, dtype, shape):
 
 def _on_gpu(t):
     return t.is_cuda
+
+
+def _table(name, pt, B, T):
+    """(address, row length) of a page table for B sequences of up to T tokens; None: none."""
+    if pt is None:
+        return None
+    shape = pt.shape
+    if (len(shape) != 2 or shape[0] < B or shape[1] * BLOCK < T or pt.dtype is not _I32 or
+            not pt.is_contiguous()):
+        raise BsaError(f"{name}: a contiguous int32 page table of {B} rows and {-(-T // BLOCK)} "
+                       f"pages a row at least wanted, got {pt.dtype} {tuple(shape)} with strides "
+                       f"{pt.stride()}")
+    return pt.data_ptr(), shape[1]
+
+
+_NO_CACHE = CCache()
+
+
+def _structs(tok, k, v, x=None):
+    """The structs of a call's caches of keys, values and index keys (None: none), most of which
+    share a page table."""
+    pt = k.page_table
+    table = _table("k", pt, tok.B, tok.T)
+    ks = k._struct(table)
+    vs = v._struct(table if v.page_table is pt else _table("v", v.page_table, tok.B, tok.T))
+    if x is None:
+        return ks, vs, _NO_CACHE
+    return ks, vs, x._struct(table if x.page_table is pt else
+                             _table("k_idx", x.page_table, tok.B, tok.T))
 
 
 _NO_ROWS = CRows(None, 0, 0, 0)
@@ -616,8 +649,7 @@ def bsa_append_kv(tok: Tokens, k, v, k_cache: Cache, v_cache: Cache, k_idx=None,
         _check_device(dev, kidx_cache.tensor, kidx_cache.page_table)
     _launch(load_library().bsa_append_kv, "bsa_append_kv", dev, c,
             _rows("k", k, N, H, d, dev), _rows("v", v, N, H, d, dev),
-            _rows("k_idx", k_idx, N, H, tok.r, dev), k_cache._struct(), v_cache._struct(),
-            CCache() if kidx_cache is None else kidx_cache._struct(),
+            _rows("k_idx", k_idx, N, H, tok.r, dev), *_structs(tok, k_cache, v_cache, kidx_cache),
             _rows("q", q, N, tok.Hq, d, dev), _rows("q_out", q_out, N, tok.Hq, d, dev, True),
             None if dev_status is None else dev_status.data_ptr(), _raw_stream(stream, dev))
 
@@ -654,7 +686,7 @@ def _packed_call(name, tok, q, k, v, own, o, lse, o_f32, workspace, dev_status, 
         if stride[0] != Hq * d:
             c = CTokens.from_buffer_copy(c)
             c.q_stride = stride[0]
-    args = [c, q.data_ptr(), k._struct(), v._struct()]
+    args = [c, q.data_ptr(), *_structs(tok, k, v)[:2]]
     if own:
         _want("o_own", own[0], torch.float32, (N, Hq, d))
         _want("lse_own", own[1], torch.float32, (N, Hq))

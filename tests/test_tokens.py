@@ -383,3 +383,37 @@ def test_appends_check_values_and_index_keys_too(lib):
         assert app(ctypes.byref(tokens(**kw)), rows(), rows(), NONE, cache(T=64, head_stride=0, seq_stride=0,
                    extent=1 << 20), large, bsa.CCache(), NONE, NONE, None,
                    None) == bsa.BSA_ERR_UNSUPPORTED
+
+
+def test_page_tables_are_checked_before_a_call(monkeypatch):
+    """A table of too few rows, of another type or with rows apart would be read past its end or
+    as other pages."""
+    seen = []
+    monkeypatch.setattr(bsa, "_launch", lambda fn, what, dev, *args: seen.append(what))
+    monkeypatch.setattr(bsa, "_rows", lambda *a: None)
+    monkeypatch.setattr(bsa, "_raw_stream", lambda *a: 0)
+    pool = torch.zeros(5, 2, 64, 64, dtype=torch.bfloat16)
+    idx = torch.zeros(5, 2, 64, 16, dtype=torch.bfloat16)
+    table = torch.zeros(3, 4, dtype=torch.int32)
+    tok = bsa.Tokens(N=3, B=3, Hq=4, Hkv=2, d=64, T=256)
+    x = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+
+    def make(pool, t):
+        c = bsa.paged_cache(pool, table)
+        c.page_table = t
+        return c
+
+    append = lambda k, v, i: bsa.bsa_append_kv(tok, x, x, make(pool, k), make(pool, v), x,
+                                               make(idx, i))
+    append(table, table, table)
+    append(torch.zeros(4, 4, dtype=torch.int32), table, table)
+    assert seen == ["bsa_append_kv"] * 2
+    for bad in (table[:2], table.long(), torch.zeros(3, 8, dtype=torch.int32)[:, :4], table[0],
+                table[:, :3].contiguous()):
+        for three in ((bad, table, table), (table, bad, table), (table, table, bad)):
+            with pytest.raises(bsa.BsaError, match="page table"):
+                append(*three)
+    for bad in (table[:2], table.long()):       # the attention calls' caches go the same way
+        for two in ((bad, table), (table, bad)):
+            with pytest.raises(bsa.BsaError, match="page table"):
+                bsa._structs(tok, *(make(pool, t) for t in two))
