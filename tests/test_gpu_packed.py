@@ -747,3 +747,30 @@ def test_bad_value_pages_of_a_table_with_rows_of_its_own(new):
         1, 0, 2, 3).reshape(Hkv, -1, d)[:, :m]
     hide = lambda b, j: (j // 64 == 35) if b == 1 else np.zeros(len(j), bool)
     check(step, exact(q, mem, cu, [n, n], True, G, hide=hide), n, d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1 << 20, 1 << 17])
+def test_sums_of_many_equal_scores_behind_a_larger_one(n, d):
+    """So many rows that no unit is split. Every key behind the first has the same score, so that
+    each of n equal terms is added to a sum that has grown: lse is off by at most 2.8e-6 (an
+    exponential), 2^-21 (its argument and the ex2), 64 2^-24 (a step's sum), 2^-23 (their sum) and
+    2^-22 of itself, less than 2^-16 together at any length."""
+    G, Hkv, N = 16, 8, 16 * 74
+    K = torch.zeros(2, Hkv, 64, d, device="cuda", dtype=torch.bfloat16)
+    K[..., :8] = 0.25 * torch.arange(8, device="cuda").to(torch.bfloat16)
+    K[0, :, 0] *= 1.125
+    V = randn(2, Hkv, 64, d, seed=140)
+    pt = torch.ones(1, n // 64, dtype=torch.int32)
+    pt[0, 0] = 0
+    q = torch.zeros(N, Hkv * G, d, device="cuda", dtype=torch.bfloat16)
+    q[..., :8] = randn(N, 1, 8, seed=141)
+    scale = 0.7
+    tok = bsa.Tokens(N=N, B=1, Hq=Hkv * G, Hkv=Hkv, d=d, T=n, attn_scale=scale)
+    step = bsa.SharedPrefixDecode(tok, keep_f32=False)
+    assert bsa.bsa_packed_workspace_size(tok, bsa.OP_DECODE_SHARED) < 1 << 20     # no splits
+    step.run(q, bsa.paged_cache(K, pt.cuda()), bsa.paged_cache(V, pt.cuda()))
+    assert int(step.status.item()) == 0
+    first, other = (f64(q[:, 0, :8]) @ f64(K[0, 0, r, :8]) * float(np.float32(scale)) for r in (0, 1))
+    want = np.logaddexp(first, np.log(n - 1.0) + other)
+    assert (np.abs(f64(step.lse) - want[:, None]) <= 2.0 ** -16).all(), np.abs(f64(step.lse) - want[:, None]).max()
