@@ -1287,7 +1287,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ring = (ring + (U.ntok <= half_tok ? n : 2 * n)) % 3;
           buf = ring + t < 3 ? ring + t : 0;
         }
-        bars->ml[t][row] = make_float2(m, l);
+        // A score beyond fp32 makes its row NaN, as inf - inf does in ex2 (exp2_poly has 0 there).
+        bars->ml[t][row] = make_float2(m, m == INFINITY ? NAN : l);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->ml_full[t]);
       }

@@ -774,3 +774,20 @@ def test_sums_of_many_equal_scores_behind_a_larger_one(n, d):
     first, other = (f64(q[:, 0, :8]) @ f64(K[0, 0, r, :8]) * float(np.float32(scale)) for r in (0, 1))
     want = np.logaddexp(first, np.log(n - 1.0) + other)
     assert (np.abs(f64(step.lse) - want[:, None]) <= 2.0 ** -16).all(), np.abs(f64(step.lse) - want[:, None]).max()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [1, 70])
+def test_scores_beyond_fp32_make_their_rows_nan(d, new):
+    """inf - inf is NaN in 32 bits, wherever in a step the key is; rows without one stay."""
+    G, Hkv, n = 2, 1, 300
+    for key in (0, 13, 14, 15, 130, 229):
+        mem = Paged([n], Hkv, d, seed=150)
+        q = randn(new, G, d, seed=151)
+        q[:, 0] = 0.0
+        want = run_attend(q, mem, [0, new], [n], Hkv)
+        mem.K[int(mem.pt[0, key // 64]), 0, key % 64, 0] = 2.0 ** 100
+        q[:, 1, 0] = 2.0 ** 100
+        step = run_attend(q, mem, [0, new], [n], Hkv)
+        for x, y in ((step.o, want.o), (step.o_f32, want.o_f32), (step.lse, want.lse)):
+            assert torch.isnan(x[:, 1]).all() and torch.equal(x[:, 0], y[:, 0])
