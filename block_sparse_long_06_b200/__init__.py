@@ -86,7 +86,8 @@ class CTokens(ctypes.Structure):
                 ("rope_factor", ctypes.c_float), ("norm", ctypes.c_int32),
                 ("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p),
                 ("k_weight", ctypes.c_void_p), ("causal", ctypes.c_int32),
-                ("attn_scale", ctypes.c_float), ("q_stride", ctypes.c_int64)]
+                ("attn_scale", ctypes.c_float), ("q_stride", ctypes.c_int64),
+                ("p_parts", ctypes.c_int32)]
 
 
 _lib = None
@@ -381,6 +382,7 @@ class Tokens:
     q_stride: int = 0                          # elements between tokens of q; 0 -> Hq * d
     r: int = 16
     block: int = BLOCK
+    p_parts: int = 0                           # bf16 parts of a softmax weight (1, 2); 0 -> by rows
 
     _kept = None                               # the last call's description, not part of the state
 
@@ -440,7 +442,7 @@ class Tokens:
                        None, None, None, None, dim, int(rope is not None and rope.interleaved),
                        1.0 if rope is None else float(rope.factor), int(self.norm),
                        float(self.eps), None, None, int(self.causal), float(self.attn_scale),
-                       int(self.q_stride))
+                       int(self.q_stride), int(self.p_parts))
 
 
 _ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}

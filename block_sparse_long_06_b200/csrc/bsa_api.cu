@@ -215,6 +215,7 @@ bsa_status_t check_tokens(const bsa_tokens_t* t) {
   if (t->rope_dim < 0 || t->rope_dim > t->d || (t->rope_dim > 0 && t->rope_steps == nullptr))
     return BSA_ERR_INVALID_ARG;
   if (t->q_stride < 0 || t->q_stride % 8 != 0) return BSA_ERR_INVALID_ARG;
+  if (t->p_parts < 0 || t->p_parts > 2) return BSA_ERR_INVALID_ARG;
   if (t->block != 64 || t->r != 16) return BSA_ERR_UNSUPPORTED;
   if (t->d != 64 && t->d != 128) return BSA_ERR_UNSUPPORTED;
   if (t->rope_dim % 16 != 0) return BSA_ERR_UNSUPPORTED;
@@ -445,6 +446,11 @@ bsa_status_t packed_attention(const bsa_tokens_t* t, bool shared, const void* q,
   a.v_safe = inside_extent(v, t);
   a.scale_log2 = (t->attn_scale > 0.f ? t->attn_scale : 1.0f / std::sqrt(static_cast<float>(t->d))) *
                  1.4426950408889634f;
+  // With no more rows than fill a tile a sequence, the keys' arrival takes the time (one row each
+  // of 8 sequences over 32K keys: 136 us with one part, 148 with two), with more the products do
+  // (a prompt of 32K: 7.8 and 10.4 ms).
+  const bool few = static_cast<int64_t>(t->N) * a.G <= 128ll * t->B;
+  a.p_parts = t->p_parts != 0 ? t->p_parts : few ? 2 : 1;
   const cudaError_t e = bsa::launch_packed(a, tq, tk, tv, num_sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? BSA_OK : cuda_fail(e);
 }

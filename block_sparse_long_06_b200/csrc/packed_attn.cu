@@ -16,14 +16,18 @@
 //  * A step is 128 keys (two blocks of the cache). The loader warp copies K and V of a step
 //    into a ring of 32 KB stages; one issuing thread runs S = Q K^T into 128 columns of tensor
 //    memory and O += P V from them; four softmax warps per tile, a thread a row, turn S into P,
-//    written as bf16 over S. The two tiles take turns: while one is in its softmax, the other
-//    has the tensor cores. P V (j) and S (j + 1) of a tile are issued by the same thread, in
-//    order, so S needs no second buffer and the arrival of S (j + 1) says that P V (j) is done.
+//    written as bf16 over S and handed over by quarters. The two tiles take turns: while one is
+//    in its softmax, the other has the tensor cores. P V (j) and S (j + 1) of a tile are issued
+//    by the same thread, in order, so S needs no second buffer and the arrival of S (j + 1) says
+//    that P V (j) is done.
 //    (At d = 64 there is room for a third buffer of scores, and S runs further ahead.)
 //  * The running maximum only moves when it grows by more than 8 (log2): O is then rescaled
-//    in tensor memory. P <= 2^8 is rounded to bf16 (at most 2^-8 of each term, as much as the
-//    output's own rounding, and averaged over a row's terms); l sums the fp32 values. V stays
-//    bf16, so no value range is lost.
+//    in tensor memory. l sums the fp32 weights, P <= 2^8. P meets V as one bf16 part, off by
+//    2^-8 of itself at most (as the output's own rounding is; where one key dominates a row, by
+//    that of the result), or as two, in both halves of S's columns, off by 2^-15. Two are half as
+//    many products again: a prompt of 32K takes 10.4 ms instead of 7.8, 200 rows behind three
+//    prefixes of 64K 460 us instead of 370, but one row each over 32K keys 148 instead of 136,
+//    since there the keys' arrival takes the time. V stays bf16, so no value range is lost.
 //  * Four more warps write a unit's result from tensor memory while the softmax warps are in
 //    the next unit's first steps (with the softmax warps writing it, 10,000 cycles a unit).
 //  * Few rows over many keys: a plan (a kernel of one block or, for few tiles, each block for
@@ -94,7 +98,7 @@ struct Bars {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], kv_raw[kMaxStages];
   uint64_t s_full[2][3];               // [tile][buffer]
   uint64_t pv_done[2], o_full[2];      // pv_done: with three buffers
-  uint64_t p_ready[3][2];              // [buffer][half of the step's keys]
+  uint64_t p_ready[3][4];              // [buffer][quarter of the step's keys]
   uint64_t ml_full[2], o_empty[2];     // a unit's (m, l) is written; its O and (m, l) are read
   uint64_t mma_done;
   float2 ml[2][128];                   // [tile][row]
@@ -674,7 +678,7 @@ BSA_DEVFN void out_role(const PackedArgs& a, Bars* bars, uint32_t tmem) {
 }
 
 // ------------------------------------------------------------------------------- main
-template <int D>
+template <int D, int kParts>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_attn_kernel(const PackedArgs a, const __grid_constant__ CUtensorMap tmq,
                        const __grid_constant__ CUtensorMap tmk,
@@ -699,6 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int b = 0; b < 3; ++b) {
         mbar_init(&bars->s_full[x][b], 1);
         mbar_init(&bars->p_ready[b][x], 4);  // the tile's softmax warps
+        mbar_init(&bars->p_ready[b][x + 2], 4);
       }
       mbar_init(&bars->pv_done[x], 1);
       mbar_init(&bars->ml_full[x], 4);
@@ -1002,7 +1007,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc::commit(&bars->s_full[t][C::kRing == 2 ? 0 : b]);
       };
-      // O of tile t += P V, P (buffer b) in two parts as the softmax hands them over
+      // O of tile t += P V, P (buffer b) by quarters of the keys as the softmax hands them over
       auto values = [&](int t, int b, const Pos& p, bool first) {
         const uint32_t s_tm = tmem + C::kScores + 128 * b, o_tm = tmem + D * t;
         const uint32_t phase = (p_phase >> b) & 1;
@@ -1010,16 +1015,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t dv = dv0 + (((p.st - more) * C::kTile) >> 4);
         keep(dv);
         if (first && !mbar_wait(&bars->o_empty[t], o_phase)) return false;
-        if (!mbar_wait(&bars->p_ready[b][0], phase) || !full(p)) return false;
-        tc::fence_after_sync();
+        if (!full(p)) return false;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          tc::mma_ts(o_tm, s_tm + kk * 8, dv + ((kk * 2048) >> 4), idPV, !first || kk > 0);
-        if (!mbar_wait(&bars->p_ready[b][1], phase)) return false;
-        tc::fence_after_sync();
+        for (int i = 0; i < 4; ++i) {
+          if (!mbar_wait(&bars->p_ready[b][i], phase)) return false;
+          tc::fence_after_sync();
 #pragma unroll
-        for (int kk = 4; kk < 8; ++kk)
-          tc::mma_ts(o_tm, s_tm + kk * 8, dv + ((kk * 2048) >> 4), idPV, true);
+          for (int kk = 2 * i; kk < 2 * i + 2; ++kk) {
+            tc::mma_ts(o_tm, s_tm + kk * 8, dv + ((kk * 2048) >> 4), idPV, !first || kk > 0);
+            if constexpr (kParts == 2)
+              tc::mma_ts(o_tm, s_tm + kStep / 2 + kk * 8, dv + ((kk * 2048) >> 4), idPV, true);
+          }
+        }
         return true;
       };
       auto query = [&](int t) {
@@ -1053,7 +1060,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           for (int i0 = 0; i0 < total && ok; i0 += 2) {
-#pragma unroll
+#pragma unroll 1
             for (int t = 0; t < 2; ++t) {
               const int i = i0 + t, q = one ? 0 : t;
               if (i >= total) break;
@@ -1176,8 +1183,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (C::kRing == 3) buf = buf == 0 ? 2 : buf - 1;     // two pairs on
         if (idle) {   // rows of P that nobody reads
           if (lane == 0) {
-            mbar_arrive(&ready[0]);
-            mbar_arrive(&ready[1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mbar_arrive(&ready[i]);
           }
           continue;
         }
@@ -1245,24 +1252,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 neg2 = make_float2(neg, neg), sc2 = make_float2(sc, sc);
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {   // the P V of the first 64 keys starts after the first half
+        for (int i = 0; i < 4; ++i) {   // the P V of 32 keys starts when they are written
+          uint32_t hi[16], lo[16];
 #pragma unroll
-          for (int i = 2 * h; i < 2 * h + 2; ++i) {
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              const float2 v = __ffma2_rn(
-                  make_float2(__uint_as_float(s[i][c]), __uint_as_float(s[i][c + 1])), sc2, neg2);
-              const float2 p = (c / 2) % kPolyOf >= kPolyOf - C::kPoly
-                                   ? exp2_poly(v) : make_float2(ex2(v.x), ex2(v.y));
-              sum = __fadd2_rn(sum, p);
-              s[i >> 1][(i & 1) * 16 + c / 2] = pack_bf16(p.x, p.y);
+          for (int c = 0; c < 32; c += 2) {
+            const float2 v = __ffma2_rn(
+                make_float2(__uint_as_float(s[i][c]), __uint_as_float(s[i][c + 1])), sc2, neg2);
+            const float2 p = (c / 2) % kPolyOf >= kPolyOf - C::kPoly
+                                 ? exp2_poly(v) : make_float2(ex2(v.x), ex2(v.y));
+            sum = __fadd2_rn(sum, p);
+            if constexpr (kParts == 2) {   // the leading 8 bits, and the rest rounded to 8 more
+              const uint32_t x = __float_as_uint(p.x), y = __float_as_uint(p.y);
+              const float2 rest = __fadd2_rn(p, make_float2(-__uint_as_float(x & 0xffff0000u),
+                                                            -__uint_as_float(y & 0xffff0000u)));
+              hi[c / 2] = __byte_perm(x, y, 0x7632);
+              lo[c / 2] = pack_bf16(rest.x, rest.y);
+            } else {
+              hi[c / 2] = pack_bf16(p.x, p.y);
             }
           }
-          tc::st32(s_col + 32 * h, s[h]);
+          st16(s_col + 16 * i, hi);
+          if constexpr (kParts == 2) st16(s_col + kStep / 2 + 16 * i, lo);
           tc::wait_st();
           tc::fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&ready[h]);
+          if (lane == 0) mbar_arrive(&ready[i]);
         }
         // A step's sum joins l with what the last one lost in the rounding (Kahan's summation): l is
         // within 64 2^-24 of the sum of its terms at any length. Added one by one to two running sums,
@@ -1393,14 +1407,14 @@ __global__ void __launch_bounds__(kMergeThreads) packed_merge_kernel(const Packe
   }
 }
 
-template <int D>
+template <int D, int kParts>
 cudaError_t launch_d(const PackedArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
                      const CUtensorMap& tv, int num_sms, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (!a.in_block) e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a);
   if (e != cudaSuccess) return e;
   constexpr int smem = smem_bytes<D>();
-  auto kern = packed_attn_kernel<D>;
+  auto kern = packed_attn_kernel<D, kParts>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t units = static_cast<int64_t>(a.max_entries) * a.Hkv;
@@ -1418,7 +1432,9 @@ cudaError_t launch_d(const PackedArgs& a, const CUtensorMap& tq, const CUtensorM
 
 cudaError_t launch_packed(const PackedArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
                           const CUtensorMap& tv, int num_sms, cudaStream_t s) {
-  return a.d == 128 ? launch_d<128>(a, tq, tk, tv, num_sms, s) : launch_d<64>(a, tq, tk, tv, num_sms, s);
+  if (a.p_parts == 2)
+    return a.d == 128 ? launch_d<128, 2>(a, tq, tk, tv, num_sms, s) : launch_d<64, 2>(a, tq, tk, tv, num_sms, s);
+  return a.d == 128 ? launch_d<128, 1>(a, tq, tk, tv, num_sms, s) : launch_d<64, 1>(a, tq, tk, tv, num_sms, s);
 }
 
 }  // namespace bsa

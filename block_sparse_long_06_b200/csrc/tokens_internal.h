@@ -52,6 +52,7 @@ struct PackedArgs {
   int max_entries, num_sms, lgG;   // lgG: log2(G)
   int k_safe, v_safe;         // every page (or block) of the cache lies inside its extent
   float scale_log2;
+  int p_parts;                // bf16 parts of P: 1 or 2
 };
 
 cudaError_t launch_token_heads(const HeadsArgs& a, int num_sms, cudaStream_t s);

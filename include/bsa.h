@@ -333,6 +333,11 @@ typedef struct {
   float attn_scale;          /* softmax scale; 0 = 1/sqrt(d) */
   int64_t q_stride;          /* attention: elements between the query rows of two tokens
                                 (a multiple of 8, at least Hq*d); 0 = Hq*d */
+  int32_t p_parts;           /* attention: bf16 parts of a softmax weight where it meets V.
+                                1: it is rounded to bf16, by 2^-8 of itself at most; 2: by
+                                2^-15, for half as many products again; 0: 2 where
+                                N * Hq/Hkv <= 128 * B (decode: the keys' arrival takes the
+                                time), else 1 */
 } bsa_tokens_t;
 
 /* Head norm and rotary positions. For each row and each head of q and k (width d):
@@ -361,10 +366,13 @@ bsa_status_t bsa_append_kv(const bsa_tokens_t* tok, bsa_rows_t k, bsa_rows_t v, 
  * sequence b sees its tokens 0 .. token(i) (causal) or 0 .. seq_lens[b]-1.
  * q [N, Hq, d] bf16 (tok->q_stride); k, v caches (width d).
  * Outputs: o [N, Hq, d] bf16, lse [N, Hq] fp32 (natural log; -inf and o = 0 where a
- * row sees nothing), o_f32 [N, Hq, d] fp32 or NULL. K and V of a sequence's own tokens
- * have to be finite; what lies behind them in the last page may be anything. A block
- * with a bad page is left out and reported. Where cu_seqlens is bad nothing is written.
- * Workspace: bsa_packed_workspace_size. */
+ * row sees nothing), o_f32 [N, Hq, d] fp32 or NULL: o before its rounding. Scores, weights
+ * and all sums are fp32; a weight is rounded where it meets V (tok->p_parts), so that o_f32
+ * is off by up to 2^-8 or 2^-15 of the weighted mean of |v|; lse does not depend on it. q,
+ * and K and V of a sequence's own tokens, have to be finite; what lies behind them in the
+ * last page may be anything. A score beyond fp32 makes its row NaN. A block with a bad
+ * page is left out and reported. Where cu_seqlens is bad nothing is written. Workspace:
+ * bsa_packed_workspace_size. */
 bsa_status_t bsa_attend_packed(const bsa_tokens_t* tok, const void* q, bsa_cache_t k,
                                bsa_cache_t v, void* o, float* lse, float* o_f32, void* workspace,
                                size_t workspace_bytes, int32_t* dev_status, void* stream);

@@ -791,3 +791,76 @@ def test_scores_beyond_fp32_make_their_rows_nan(d, new):
         step = run_attend(q, mem, [0, new], [n], Hkv)
         for x, y in ((step.o, want.o), (step.o_f32, want.o_f32), (step.lse, want.lse)):
             assert torch.isnan(x[:, 1]).all() and torch.equal(x[:, 0], y[:, 0])
+
+
+# ------------------------------------------------------------------ weights in one or two parts
+def check_parts(step, want, keys, d, parts):
+    """As check, with weights that are off by 2^-8 (one part) or 2^-15 (two) where they meet V."""
+    o, lse, spread, size = want
+    live = ~np.isnan(lse)
+    e = d * 2.0 ** -23 * size + 2.0 ** -17
+    bound = ((2.0 ** -8 if parts == 1 else 2.0 ** -15) + 2 * e + keys * 2.0 ** -23)[..., None] * spread
+    off = np.abs(f64(step.o_f32) - o)
+    assert (off <= bound)[live].all(), float((off - bound)[live].max())
+    check(step, want, keys, d)
+
+
+@pytest.mark.parametrize("d,G", [(64, 1), (64, 8), (128, 4), (128, 16)])
+@pytest.mark.parametrize("parts", [0, 1, 2])
+@pytest.mark.parametrize("rows,lens", [([1, 1, 1], [3000, 64, 1]), ([90, 2, 33], [700, 1500, 129])])
+def test_weights_in_one_or_two_parts(d, G, parts, rows, lens):
+    """Two where a call's rows fill no more than a tile a sequence, unless the caller says."""
+    Hkv = 2
+    cu = sums(rows)
+    mem = Paged(lens, Hkv, d, seed=160)
+    q = randn(cu[-1], Hkv * G, d, seed=161, scale=1.5)
+    step = run_attend(q, mem, cu, lens, Hkv, p_parts=parts)
+    want = exact(q, mem, cu, lens, True, G)
+    few = cu[-1] * G <= 128 * len(lens)
+    got = parts or (2 if few else 1)
+    check_parts(step, want, max(lens), d, got)
+    for other in (1, 2):
+        same = torch.equal(run_attend(q, mem, cu, lens, Hkv, p_parts=other).o_f32, step.o_f32)
+        assert same == (other == got)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows,lens", [([40, 1], [5000, 300]), ([200, 90], [700, 2600])])
+def test_shared_prefixes_join_parts_of_one_precision(d, rows, lens):
+    """As exact as the own parts that bsa_decode gives, where the caller asks for it or the rows
+    are few; the own part's weight may be all but nothing, or all."""
+    G, Hkv = 4, 2
+    cu = sums(rows)
+    mem = Paged(lens, Hkv, d, seed=162)
+    q = randn(cu[-1], Hkv * G, d, seed=163, scale=1.5)
+    own = (torch.randn(cu[-1], Hkv * G, d, generator=gen(164), device="cuda"),
+           8.0 + 6.0 * torch.randn(cu[-1], Hkv * G, generator=gen(165), device="cuda"))
+    tok = bsa.Tokens(N=cu[-1], B=2, Hq=Hkv * G, Hkv=Hkv, d=d, T=mem.T, cu_seqlens=ints(cu),
+                     seq_lens=ints(lens), p_parts=2)
+    step = bsa.SharedPrefixDecode(tok)
+    step.run(q, *mem.caches(), *own)
+    assert int(step.status.item()) == 0
+    check_parts(step, exact_shared(q, mem, cu, lens, G, own), max(lens), d, 2)
+
+
+@pytest.mark.parametrize("parts", [1, 2])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows,lens,causal", [([1, 1], [5000, 700], True), ([300, 1, 70], [900, 64, 1000], True),
+                                              ([17], [333], False), ([130] * 40, [200 + 3 * b for b in range(40)], False)])
+def test_every_row_of_v_counts(parts, d, rows, lens, causal):
+    """With q = 0 all weights are 1 and a row's result is the mean of the n values it sees, from
+    n / 16 sums of 16 products each, off by 2^-22 at most of the sizes added up (and 20 steps for
+    parts and the division): not one key may be missing or counted twice, which is 1 / n."""
+    G, Hkv = 4, 2
+    cu = sums(rows)
+    mem = Paged(lens, Hkv, d, seed=166)
+    q = torch.zeros(cu[-1], Hkv * G, d, dtype=torch.bfloat16, device="cuda")
+    step = run_attend(q, mem, cu, lens, Hkv, causal, p_parts=parts)
+    for b, n in enumerate(lens):
+        V = mem.keys(mem.V, b, n)
+        total, size = np.cumsum(V, 1), np.cumsum(np.abs(V), 1)
+        seen = np.arange(n - rows[b], n) if causal else np.full(rows[b], n - 1)
+        mean, size = (np.repeat(x[:, seen].transpose(1, 0, 2), G, 1) / (seen + 1.0)[:, None, None]
+                      for x in (total, size))
+        off = np.abs(f64(step.o_f32[cu[b]:cu[b + 1]]) - mean)
+        assert (off <= (n / 8 + 20) * 2.0 ** -23 * size).all(), float((off / size).max())

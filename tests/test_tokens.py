@@ -417,3 +417,9 @@ def test_page_tables_are_checked_before_a_call(monkeypatch):
         for two in ((bad, table), (table, bad)):
             with pytest.raises(bsa.BsaError, match="page table"):
                 bsa._structs(tok, *(make(pool, t) for t in two))
+
+
+@pytest.mark.parametrize("parts", [-1, 3])
+def test_parts_of_a_weight_are_one_or_two(lib, parts):
+    assert lib.bsa_attend_packed(ctypes.byref(tokens(p_parts=parts)), 0x10000, cache(), cache(), 0x20000,
+                                 0x30000, None, 0x100000, 1 << 40, None, None) == bsa.BSA_ERR_INVALID_ARG
