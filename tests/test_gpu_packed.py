@@ -846,7 +846,8 @@ def test_shared_prefixes_join_parts_of_one_precision(d, rows, lens):
 @pytest.mark.parametrize("parts", [1, 2])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("rows,lens,causal", [([1, 1], [5000, 700], True), ([300, 1, 70], [900, 64, 1000], True),
-                                              ([17], [333], False), ([130] * 40, [200 + 3 * b for b in range(40)], False)])
+                                              ([17], [333], False), ([130] * 40, [200 + 3 * b for b in range(40)], False),
+                                              ([700, 220, 500, 640], [4500, 1500, 2500, 700], True)])
 def test_every_row_of_v_counts(parts, d, rows, lens, causal):
     """With q = 0 all weights are 1 and a row's result is the mean of the n values it sees, from
     n / 16 sums of 16 products each, off by 2^-22 at most of the sizes added up (and 20 steps for
@@ -864,3 +865,46 @@ def test_every_row_of_v_counts(parts, d, rows, lens, causal):
                       for x in (total, size))
         off = np.abs(f64(step.o_f32[cu[b]:cu[b + 1]]) - mean)
         assert (off <= (n / 8 + 20) * 2.0 ** -23 * size).all(), float((off / size).max())
+
+
+# ------------------------------------------------------------------ the plan kernel's own cases
+PLAN_KERNEL = [
+    # new, lens, Hkv, G, d, causal, the kernel plans, some unit is cut
+    ([1] * 32, [1 + 83 * b for b in range(32)], 2, 4, 128, True, False, None),   # 32 tiles
+    ([1] * 33, [1 + 83 * b for b in range(33)], 2, 4, 128, True, True, True),    # 33
+    ([600], [1500], 49, 1, 64, True, False, None),       # 3 tiles of 49 heads, 147 units, and of 50
+    ([600], [1500], 50, 1, 64, True, True, False),
+    # 35 tiles of up to 32 tokens, most of them two tiles of rows, over long and short contexts
+    ([400, 100, 250, 300], [4500, 1500, 2500, 700], 1, 8, 64, True, True, True),
+    ([400, 100, 250, 300], [4500, 1500, 2500, 700], 1, 8, 64, False, True, True),
+    ([400, 100, 250, 300], [4500, 1500, 2500, 700], 1, 8, 128, True, True, True),
+    ([400, 100, 250, 300], [4500, 1500, 2500, 700], 1, 8, 128, False, True, True),
+    # the same between sequences without rows or without tokens, rows of one tile among them
+    # (763 rows of 6 sequences make 29 tiles at most, 963 make 35)
+    ([0, 333, 7, 0, 420, 1], [900, 3001, 4000, 0, 2111, 77], 2, 8, 128, True, False, None),
+    ([0, 433, 7, 0, 520, 1], [900, 3001, 4000, 0, 2111, 77], 2, 8, 128, True, True, True),
+]
+
+
+@pytest.mark.parametrize("new,lens,Hkv,G,d,causal,kernel,cut", PLAN_KERNEL)
+def test_the_plan_kernel_cuts_units_of_one_and_two_tiles(new, lens, Hkv, G, d, causal, kernel, cut):
+    """Which way a call is planned shows in the first words of its workspace: the plan kernel writes
+    the number of entries, and whether a tile has several."""
+    assert torch.cuda.get_device_properties(0).multi_processor_count == 148    # what the cases count on
+    cu = sums(new)
+    mem = Paged(lens, Hkv, d, seed=170)
+    q = randn(cu[-1] + 2, Hkv * G, d, seed=171, scale=1.5)
+    tok = bsa.Tokens(N=cu[-1] + 2, B=len(lens), Hq=Hkv * G, Hkv=Hkv, d=d, T=mem.T, cu_seqlens=ints(cu),
+                     seq_lens=ints(lens), causal=causal)
+    step = bsa.PackedAttention(tok)
+    step.workspace.fill_(0xff)
+    step.o_f32.fill_(77.0)
+    step.run(q, *mem.caches())
+    entries, _, any_cut, _ = step.workspace[:16].view(torch.int32).tolist()
+    assert int(step.status.item()) == 0
+    assert (entries != -1) == kernel
+    if kernel:
+        tiles = sum(-(-n // (256 // G)) for n in new)
+        assert any_cut == cut and (entries > tiles) == cut
+    assert (step.o_f32[cu[-1]:] == 77.0).all()
+    check(step, exact(q, mem, cu, lens, causal, G), max(lens), d)
