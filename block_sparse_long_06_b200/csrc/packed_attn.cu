@@ -74,11 +74,12 @@ struct Cfg {
   static constexpr int kTile = kHalves * kSlab;     // 128 rows x D: a Q tile, or K or V of a step
   // One more where no unit has two tiles: it takes the place of the second Q tile, before the
   // others. A pair of steps of one tile uses four stages, so that with five the next keys come
-  // late: 2,250 cycles a step at d = 128 (keys in L2), 1,650 with six; from HBM 2,970 and 2,760.
+  // late: 2,250 cycles a step at d = 128 (keys in L2), 1,650 with six; from HBM 2,970 and 2,760
+  // (the loop of steps alone; see step_cost for whole calls).
   static constexpr int kStages = D == 128 ? 5 : 10;
   // Of every kPolyOf pairs of a row's scores, kPoly take their exponentials by polynomial. At
-  // d = 128 more cost power, which is the limit there; at d = 64 a step of two tiles takes 2,650
-  // cycles with none, 2,730 with 1, 2,610 with 2 and 3,150 with 3.
+  // d = 128 more cost power, which is the limit there; at d = 64 the loop of steps of two tiles
+  // takes 2,650 cycles a step with none, 2,730 with 1, 2,610 with 2 and 3,150 with 3.
   static constexpr int kPoly = D == 128 ? 1 : 2;
   // Buffers of scores: one a tile, or three that the tiles take in turn (see the issuer).
   static constexpr int kRing = D == 128 ? 2 : 3;
@@ -145,7 +146,7 @@ BSA_DEVFN float max3(float x, float y, float z) {
 // 2^x on the FMA pipes, two lanes at once, for x <= 8: x = n + f with n the nearest integer
 // (adding 1.5 * 2^23 rounds it into the low mantissa bits), 2^f by a quartic of least relative
 // error on [-1/2, 1/2] among those that are exactly 1 at 0 (Remez exchange, exp2_poly_fit.py:
-// 2.8e-6; the bf16 P needs 2^-9), n added to the exponent field.
+// 2.8e-6, below 2^-18), n added to the exponent field.
 // x is clamped at -127, where that gives exactly 0: masked scores add nothing.
 BSA_DEVFN float2 exp2_poly(float2 x) {
   constexpr float kC1 = 0.6931241750717163f, kC2 = 0.24024099111557007f;
@@ -190,8 +191,10 @@ BSA_DEVFN int seq_len(const PackedArgs& a, int b) {
   return a.seq_lens != nullptr ? max(0, min(a.seq_lens[b], a.T)) : a.T;
 }
 
-// What a step of a unit costs: with two tiles of rows it takes 3,010 cycles (d = 64: 2,820), with
-// one 2,250 to 2,970, which its keys take to arrive, and 1,460 at d = 64.
+// What a step of a unit costs. Calls of 148 heads of 256 rows over 32K keys take 3,350 cycles a
+// step of two tiles, starts and ends included (d = 64: 2,900), of 128 rows 1,790 where the keys are
+// in L2 and 2,620 from HBM, which is where few rows mostly find theirs (d = 64: 1,520 and 1,550).
+// With P in two parts 4,500, 2,440 and 2,450 (3,770, 1,930 and 1,930): few rows have one tile.
 BSA_DEVFN int step_cost(int d, bool two) { return two ? 4 : d == 128 ? 3 : 2; }
 
 // Without splits the SMs are evenly loaded where there are several units for each SM and the
@@ -1037,9 +1040,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Pair i is step i / 2 of tile i % 2 (the K and V of a step are used twice) or, with one
       // tile of rows, step i in tile i % 2 of tensor memory. With a buffer of scores for each
       // tile, pair i + 2 is scored behind the P V of pair i: a tile's softmax waits for it,
-      // for a part of 2,820 cycles. At d = 64 tensor memory has room for a third, which the
-      // tiles take in turn, and pair i + 3 is scored then (2,730 cycles; 1,008 rows over 9K keys,
-      // 64/4 heads, 949 us instead of 1,012). There the softmax warps' issue slots are the limit.
+      // at d = 64 for a part of 2,820 cycles a step. There tensor memory has room for a third, which
+      // the tiles take in turn, and pair i + 3 is scored then (2,730 cycles; 1,008 rows over 9K
+      // keys, 64/4 heads, 949 us instead of 1,012). What is left is latency: a prompt of 8K has its
+      // issue slots 56% busy, its exponentials' units 55%, the tensor pipe 36%.
       int ring = 0;                                // with three: the buffer of the unit's pair 0
       bool ok = fetch();
       while (ok && total > 0) {

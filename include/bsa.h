@@ -385,7 +385,8 @@ bsa_status_t bsa_attend_packed(const bsa_tokens_t* tok, const void* q, bsa_cache
  * own tokens (bsa_decode's o_f32 and lse; lse_own = -inf: none), or both NULL. The
  * outputs are the attention over prefix and own tokens together:
  *   lse = log(e^lse_p + e^lse_own),  o = e^(lse_p - lse) o_p + e^(lse_own - lse) o_own.
- * o, lse and o_f32 as in bsa_attend_packed; o_f32 may be o_own and lse may be lse_own. */
+ * o, lse and o_f32 as in bsa_attend_packed (p_parts = 2 for a prefix's part nearly as exact
+ * as bsa_decode's); o_f32 may be o_own and lse may be lse_own. */
 bsa_status_t bsa_decode_shared(const bsa_tokens_t* tok, const void* q, bsa_cache_t k,
                                bsa_cache_t v, const float* o_own, const float* lse_own, void* o,
                                float* lse, float* o_f32, void* workspace, size_t workspace_bytes,
