@@ -407,18 +407,19 @@ class Tokens:
                                                   kept[4] != (rope.interleaved, rope.factor))):
             kept = self._describe_again()
         c = kept[0]
-        for name, t, n in kept[2]:
-            if t.numel() != n:
+        for name, size, address, n in kept[2]:
+            if size() != n:
                 self._describe_again()
                 return self._description()
-            setattr(c, name, t.data_ptr())
+            setattr(c, name, address())
         return c, kept[1]
 
     def _describe_again(self):
         self._kept, rope = None, self.rope
         names = ("cu_seqlens", "seq_lens", "positions", "q_weight", "k_weight", "rope_steps")
-        given = [(n, t, t.numel()) for n, t in zip(names, self.tensors()) if t is not None]
-        self._kept = (self._describe(), given[0][1].get_device() if given else -1, given,
+        tensors = [(n, t) for n, t in zip(names, self.tensors()) if t is not None]
+        self._kept = (self._describe(), tensors[0][1].get_device() if tensors else -1,
+                      [(n, t.numel, t.data_ptr, t.numel()) for n, t in tensors],
                       None if rope is None else rope.steps,
                       None if rope is None else (rope.interleaved, rope.factor))
         return self._kept
@@ -463,7 +464,7 @@ def _on_gpu(t):
     return t.is_cuda
 
 
-def _table(name, pt, B, T):
+def _table(name, pt, B, T, dev):
     """(address, row length) of a page table for B sequences of up to T tokens; None: none."""
     if pt is None:
         return None
@@ -473,23 +474,28 @@ def _table(name, pt, B, T):
         raise BsaError(f"{name}: a contiguous int32 page table of {B} rows and {-(-T // BLOCK)} "
                        f"pages a row at least wanted, got {pt.dtype} {tuple(shape)} with strides "
                        f"{pt.stride()}")
+    if pt.get_device() != dev:
+        _check_device(dev, pt)
     return pt.data_ptr(), shape[1]
 
 
 _NO_CACHE = CCache()
 
 
-def _structs(tok, k, v, x=None):
-    """The structs of a call's caches of keys, values and index keys (None: none), most of which
-    share a page table."""
-    pt = k.page_table
-    table = _table("k", pt, tok.B, tok.T)
+def _structs(tok, dev, k, v, x=None):
+    """The structs of a call's caches of keys, values and index keys (None: none) on device `dev`,
+    most of which share a page table."""
+    B, T, pt = tok.B, tok.T, k.page_table
+    if k.tensor.get_device() != dev or v.tensor.get_device() != dev:
+        _check_device(dev, k.tensor, v.tensor)
+    table = _table("k", pt, B, T, dev)
     ks = k._struct(table)
-    vs = v._struct(table if v.page_table is pt else _table("v", v.page_table, tok.B, tok.T))
+    vs = v._struct(table if v.page_table is pt else _table("v", v.page_table, B, T, dev))
     if x is None:
         return ks, vs, _NO_CACHE
+    _check_device(dev, x.tensor)
     return ks, vs, x._struct(table if x.page_table is pt else
-                             _table("k_idx", x.page_table, tok.B, tok.T))
+                             _table("k_idx", x.page_table, B, T, dev))
 
 
 _NO_ROWS = CRows(None, 0, 0, 0)
@@ -533,7 +539,7 @@ def _raw_stream(stream, dev) -> int:
 def _launch(fn, what, dev, *args):
     """Call an entry point with `dev` as the current device (kernels and streams belong to
     it) and raise on a status."""
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         status = fn(*args)
     else:
         with torch.cuda.device(dev):
@@ -645,13 +651,11 @@ def bsa_append_kv(tok: Tokens, k, v, k_cache: Cache, v_cache: Cache, k_idx=None,
         raise BsaError("bsa_append_kv: q and q_out, k_idx and kidx_cache come together")
     dev = k.get_device()
     N, d, H, c = tok.N, tok.d, tok.Hkv, _tokens_on(tok, dev)
-    _check_device(dev, dev_status, k_cache.tensor, k_cache.page_table, v_cache.tensor,
-                  v_cache.page_table)
-    if kidx_cache is not None:
-        _check_device(dev, kidx_cache.tensor, kidx_cache.page_table)
+    if dev_status is not None:
+        _check_device(dev, dev_status)
     _launch(load_library().bsa_append_kv, "bsa_append_kv", dev, c,
             _rows("k", k, N, H, d, dev), _rows("v", v, N, H, d, dev),
-            _rows("k_idx", k_idx, N, H, tok.r, dev), *_structs(tok, k_cache, v_cache, kidx_cache),
+            _rows("k_idx", k_idx, N, H, tok.r, dev), *_structs(tok, dev, k_cache, v_cache, kidx_cache),
             _rows("q", q, N, tok.Hq, d, dev), _rows("q_out", q_out, N, tok.Hq, d, dev, True),
             None if dev_status is None else dev_status.data_ptr(), _raw_stream(stream, dev))
 
@@ -677,8 +681,7 @@ def _packed_call(name, tok, q, k, v, own, o, lse, o_f32, workspace, dev_status, 
     if dev < 0:
         raise BsaError(f"{name}: q has to be on the GPU")
     c = _tokens_on(tok, dev)
-    _check_device(dev, k.tensor, k.page_table, v.tensor, v.page_table, o, lse, o_f32, workspace,
-                  dev_status, *own)
+    _check_device(dev, o, lse, o_f32, workspace, dev_status, *own)
     _want("o", o, torch.bfloat16, (N, Hq, d))
     _want("lse", lse, torch.float32, (N, Hq))
     _want("o_f32", o_f32, torch.float32, (N, Hq, d))
@@ -688,7 +691,7 @@ def _packed_call(name, tok, q, k, v, own, o, lse, o_f32, workspace, dev_status, 
         if stride[0] != Hq * d:
             c = CTokens.from_buffer_copy(c)
             c.q_stride = stride[0]
-    args = [c, q.data_ptr(), *_structs(tok, k, v)[:2]]
+    args = [c, q.data_ptr(), *_structs(tok, dev, k, v)[:2]]
     if own:
         _want("o_own", own[0], torch.float32, (N, Hq, d))
         _want("lse_own", own[1], torch.float32, (N, Hq))

@@ -416,7 +416,7 @@ def test_page_tables_are_checked_before_a_call(monkeypatch):
     for bad in (table[:2], table.long()):       # the attention calls' caches go the same way
         for two in ((bad, table), (table, bad)):
             with pytest.raises(bsa.BsaError, match="page table"):
-                bsa._structs(tok, *(make(pool, t) for t in two))
+                bsa._structs(tok, -1, *(make(pool, t) for t in two))
 
 
 @pytest.mark.parametrize("parts", [-1, 3])
